@@ -260,6 +260,81 @@ long long tl_launch_count(void);
  * earlier call left pending when this one starts (it is cleared). */
 tl_status tl_bias_grad_noalloc(int dtype, const void* dz, int rows, int cols, float* db, void* stream);
 
+/* Attention as a call of its own, with a learned relative position bias, and
+ * its backward pass.  Per sequence b and head h:
+ *   S_ij = scale * q_i . k_j + T[bucket(j - i), h] + mask[b, j]
+ *   P = softmax over the keys j;  O = P V;  lse_i = log sum_j exp(S_ij)
+ * and backward, the probabilities recomputed from lse:
+ *   P_ij = exp(S_ij - lse_i);  D_i = dO_i . O_i;  dS_ij = P_ij (dO_i . v_j - D_i)
+ *   dQ = scale dS K;  dK = scale dS^T Q;  dV = P^T dO
+ *   dT[u, h] = sum of dS_ij over every sequence and every i, j with bucket(j - i) = u
+ * No dropout.  Scores, softmax and sums are float32; 16-bit storage rounds P
+ * and dS to the storage type for their products (tensor cores), float32
+ * storage rounds nothing.  Results are bitwise reproducible.
+ *
+ * Buckets: half of them for keys at or behind the query (bucket(x) = f(-x) for
+ * x <= 0), half for keys ahead (bucket(x) = buckets/2 + f(x)); with h =
+ * buckets/2 and e = h/2, f(n) = n for n < e, else
+ * min(h - 1, e + floor(log(n/e) / log(max_distance/e) * (h - e) + 1e-9)).
+ *
+ * Mask: NULL or (batch, seq) float32, added over the keys.  A value of -1e30
+ * or less (-inf, the lowest float) removes the key.  A query row with no key
+ * left gets O = 0 and lse = +inf, and its gradients are 0; a removed key
+ * weighs 0 in every product, so its K, V, Q, dO must be finite.  lse and O
+ * given to the backward are those of the forward.
+ *
+ * tl_heads: a (batch, seq, heads, head_dim) tensor by its element strides;
+ * the head_dim entries of one head are contiguous.  data is 16-byte aligned,
+ * and the strides of every dimension of more than one entry are multiples of
+ * 16 bytes and at least head_dim (those of one entry are ignored).  Outputs
+ * must not overlap anything else; elements between their rows are left alone.
+ * lse: (batch, heads, seq) float32, dense.  bias_table: (buckets, heads),
+ * dense, storage dtype; dtable: the same shape, float32, overwritten, or added
+ * to when `accumulate` is not 0; NULL when its gradient is not wanted.
+ * Limits: head_dim a multiple of 8 up to 128; seq from 1 up to 2^20; batch *
+ * heads * (seq rounded up to 128) <= 2^30 (TL_EUNSUPPORTED above); buckets
+ * even, 4 to 256; buckets/4 < max_distance <= 2^20; scale finite, >= 0 (0
+ * means 1/sqrt(head_dim)).
+ * workspace: tl_attention_workspace_bytes(desc, backward) bytes (0 for a
+ * description that the calls refuse), 256-byte aligned; nothing in it is kept
+ * from call to call, but calls that may overlap on the GPU need one each. */
+typedef struct {
+  int dtype;                /* tl_dtype of every tensor but mask, lse and dtable */
+  int batch, seq, heads, head_dim;
+  float scale;
+  const float* mask;
+  const void* bias_table;   /* or NULL: no bias */
+  int buckets, max_distance;
+} tl_attention;
+typedef struct {
+  void* data;
+  int64_t batch, token, head;
+} tl_heads;
+size_t tl_attention_workspace_bytes(const tl_attention* desc, int backward);
+tl_status tl_attention_forward(const tl_attention* desc, const tl_heads* q, const tl_heads* k, const tl_heads* v,
+                               const tl_heads* o, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+tl_status tl_attention_backward(const tl_attention* desc, const tl_heads* q, const tl_heads* k, const tl_heads* v,
+                                const tl_heads* o, const tl_heads* dout, const float* lse, const tl_heads* dq,
+                                const tl_heads* dk, const tl_heads* dv, float* dtable, int accumulate,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* Global gradient norm over `count` tensors of one dtype, and clipping:
+ *   norm = sqrt(sum over every tensor of g^2)
+ *   out  = g * min(1, max_norm / (norm + 1e-6)), rounded to the dtype
+ * in[i], out[i]: n[i] elements each, any alignment that the type has; out[i]
+ * is in[i] itself (in place: where the norm is within the limit nothing is
+ * written) or memory that no other tensor of the call overlaps.  norm: one
+ * float32 on the device (required).  Squares and their sum are float64, in a
+ * fixed order: bitwise reproducible.  A gradient that is not finite makes the
+ * norm infinite or NaN and the outputs follow the formula (0 or NaN).
+ * max_norm >= 0; +inf measures only (in place).  The pointer lists are read
+ * before the call returns.  workspace: tl_clip_workspace_bytes(count) bytes,
+ * 8-byte aligned, not kept from call to call; calls that may overlap on the
+ * GPU need one each. */
+size_t tl_clip_workspace_bytes(int count);
+tl_status tl_clip_grad_norm(int dtype, int count, const void* const* in, void* const* out, const uint64_t* n,
+                            float max_norm, float* norm, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Progressive Layer Dropping for a stack of layers ("Progressive Layer
  * Dropping" page, schedule section).  Host functions; no device work.
  *

@@ -1,0 +1,254 @@
+"""Attention with a relative position bias, forward and backward, on the GPU
+against the float64 reference within its elementwise bounds (attention_ref)."""
+import itertools
+import math
+
+import pytest
+import torch
+
+import attention_ref as ref
+import transformer_layer_pre_b200 as tlp
+
+pytestmark = pytest.mark.gpu
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+def _mask(kind, b, s, g):
+    if kind == "none":
+        return None
+    m = torch.zeros(b, s, dtype=torch.float32, device="cuda")
+    if kind == "lengths":
+        lens = torch.randint(1, s + 1, (b,), generator=g, device="cuda")
+        m[torch.arange(s, device="cuda")[None] >= lens[:, None]] = -math.inf
+    elif kind == "holes":
+        m[torch.rand(b, s, generator=g, device="cuda") < 0.4] = -math.inf
+    elif kind == "lowest":        # the type's lowest value, one sequence without a key
+        m[torch.rand(b, s, generator=g, device="cuda") < 0.4] = torch.finfo(torch.float32).min
+        m[0] = torch.finfo(torch.float32).min
+    elif kind == "values":
+        m = torch.randn(b, s, generator=g, device="cuda")
+    elif kind == "late":          # whole tiles of keys removed in front, one key left at the end
+        m[:, : s - 1] = -math.inf
+        m[b - 1, s // 2] = -3.0
+    elif kind == "empty":         # no key at all in the last sequence
+        m[b - 1] = -math.inf
+    return m
+
+
+def _tensors(layout, dtype, b, s, n, d, g, count):
+    """count tensors (b, s, n, d) in the layout, and what they are views of."""
+    if layout == "packed":
+        base = torch.randn(b, s, count, n, d, generator=g, device="cuda").to(dtype)
+        return list(base.unbind(2)), base
+    if layout == "bhsd":
+        base = torch.randn(count, b, n, s, d, generator=g, device="cuda").to(dtype)
+        return [t.transpose(1, 2) for t in base], base
+    assert layout == "padded"     # rows and heads with room between them
+    base = torch.randn(count, b, s + 3, n + 1, d + 8, generator=g, device="cuda").to(dtype)
+    return [t[:, :s, :n, :d] for t in base], base
+
+
+def _check(name, got, want, tol):
+    got = got.double()
+    assert torch.equal(torch.isfinite(got), torch.isfinite(want)), name
+    fine = torch.isfinite(want)
+    assert torch.equal(got[~fine], want[~fine]), name
+    off = ((got - want).abs() - tol)[fine]
+    assert off.numel() == 0 or float(off.max()) <= 0, (name, float(off.max()), float(((got - want).abs() / tol)[fine].max()))
+
+
+def _case(dtype, b, s, n, d, mask="none", buckets=32, distance=128, layout="packed", scale=None, seed=0, spread=1.0):
+    g = torch.Generator(device="cuda").manual_seed(1000 * s + 10 * d + seed)
+    dt = DT[dtype]
+    (q, k, v), _ = _tensors(layout, dt, b, s, n, d, g, 3)
+    table = (spread * torch.randn(buckets, n, generator=g, device="cuda")).to(dt) if buckets else None
+    m = _mask(mask, b, s, g)
+    kw = dict(mask=m, scale=scale)
+    own = dict(kw, bias_table=table, max_distance=distance)
+    o, lse = tlp.attention_forward(q, k, v, **own)
+    want, tol = ref.forward(q, k, v, table=table, distance=distance, **kw)
+    tlp.device_check()
+    _check("o", o, want["o"], tol["o"])
+    _check("lse", lse, want["lse"], tol["lse"])
+    do = torch.randn(b, s, n, d, generator=g, device="cuda").to(dt)
+    outs, base = _tensors(layout, dt, b, s, n, d, g, 3)
+    base.fill_(7.0)
+    dq, dk, dv, dtable = tlp.attention_backward(q, k, v, o, lse, do, **own, dq=outs[0], dk=outs[1], dv=outs[2])
+    want, tol = ref.backward(q, k, v, o, lse, do, table=table, distance=distance, **kw)
+    tlp.device_check()
+    for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
+        _check(name, t, want[name], tol[name])
+    if buckets:
+        _check("dtable", dtable, want["dtable"], tol["dtable"])
+    else:
+        assert dtable is None
+    # what lies between the rows of the outputs is left alone
+    for t in outs:
+        t.fill_(7.0)
+    assert bool((base == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("s", [1, 2, 7, 8, 31, 63, 64, 65, 127, 128, 129, 191, 193, 255, 257, 320, 513])
+def test_lengths(dtype, s):
+    _case(dtype, 2, s, 3, 64)
+    _case(dtype, 2, s, 2, 64, mask="lengths")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("d", [8, 16, 24, 32, 40, 64, 72, 80, 96, 128])
+def test_head_dims(dtype, d):
+    _case(dtype, 2, 200, 2, d)
+    _case(dtype, 1, 77, 3, d, mask="holes", buckets=16)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("mask", ["none", "lengths", "holes", "lowest", "values", "late", "empty"])
+@pytest.mark.parametrize("buckets", [0, 32])
+def test_masks(dtype, mask, buckets):
+    _case(dtype, 3, 300, 2, 64, mask=mask, buckets=buckets)
+    _case(dtype, 2, 150, 2, 128, mask=mask, buckets=buckets)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("buckets,distance", [(4, 2), (4, 1000), (8, 3), (16, 64), (32, 33), (64, 300), (128, 1024), (256, 65),
+                                              (256, 4096)])
+def test_buckets(dtype, buckets, distance):
+    """Wide tables (spread 3): a diagonal in the wrong bucket is off by whole units."""
+    _case(dtype, 1, 600, 2, 64, buckets=buckets, distance=distance, spread=3.0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("layout", ["packed", "bhsd", "padded"])
+def test_layouts(dtype, layout):
+    _case(dtype, 3, 140, 3, 64, layout=layout, mask="lengths")
+    _case(dtype, 1, 140, 1, 80, layout=layout)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("scale", [1.0, 0.01])
+def test_scale(dtype, scale):
+    _case(dtype, 2, 260, 2, 64, scale=scale, mask="values")
+
+
+def test_long_many_items():
+    """More items than the GPU holds blocks, and far more key tiles than buffers."""
+    _case("f16", 5, 130, 70, 64, mask="lengths")
+    _case("bf16", 1, 3000, 2, 64, mask="lengths")
+    _case("f16", 1, 2100, 1, 128)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_large_scores_and_growing_maximum(dtype):
+    """Keys ordered so that each tile's maximum exceeds the last by far more than the running reference allows."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    b, s, n, d = 1, 640, 2, 64
+    q = torch.ones(b, s, n, d, device="cuda").to(DT[dtype])
+    k = (torch.arange(s, device="cuda") / 64.0).floor()[None, :, None, None].expand(b, s, n, d).to(DT[dtype]).contiguous()
+    v = torch.randn(b, s, n, d, generator=g, device="cuda").to(DT[dtype])
+    for kk in (k, k.flip(1).contiguous()):
+        o, lse = tlp.attention_forward(q, kk, v, scale=0.5)
+        want, tol = ref.forward(q, kk, v, scale=0.5)
+        _check("o", o, want["o"], tol["o"])
+        _check("lse", lse, want["lse"], tol["lse"])
+
+
+def test_shared_table_accumulates():
+    g = torch.Generator(device="cuda").manual_seed(4)
+    q, k, v, do = (torch.randn(2, 100, 2, 64, generator=g, device="cuda").bfloat16() for _ in range(4))
+    table = torch.randn(32, 2, generator=g, device="cuda").bfloat16()
+    o, lse = tlp.attention_forward(q, k, v, bias_table=table)
+    one = tlp.attention_backward(q, k, v, o, lse, do, bias_table=table)[3]
+    start = torch.randn(32, 2, generator=g, device="cuda")
+    both = start.clone()
+    got = tlp.attention_backward(q, k, v, o, lse, do, bias_table=table, dtable=both, accumulate=True)[3]
+    assert got is both and float((both - (start + one)).abs().max()) <= 2.0 ** -22 * float(start.abs().max() + one.abs().max())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_repeats_bitwise_on_two_streams_and_in_a_graph(dtype):
+    g = torch.Generator(device="cuda").manual_seed(6)
+    dt = DT[dtype]
+    b, s, n, d = 3, 390, 4, 64
+    sets = []
+    for _ in range(2):
+        q, k, v, do = (torch.randn(b, s, n, d, generator=g, device="cuda").to(dt) for _ in range(4))
+        table = torch.randn(32, n, generator=g, device="cuda").to(dt)
+        sets.append((q, k, v, do, table, _mask("holes", b, s, g)))
+
+    def step(q, k, v, do, table, mask):
+        o, lse = tlp.attention_forward(q, k, v, mask=mask, bias_table=table)
+        return (o, lse) + tlp.attention_backward(q, k, v, o, lse, do, mask=mask, bias_table=table)
+
+    want = [step(*x) for x in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        got = []
+        for st, x in zip(streams, sets):
+            with torch.cuda.stream(st):
+                got.append(step(*x))
+        torch.cuda.synchronize()
+        for w, y in zip(want, got):
+            assert all(torch.equal(i, j) for i, j in zip(w, y))
+    static = [t.clone() for t in sets[0]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(*static)
+    for x, w in list(zip(sets, want)) * 2:
+        for t, src in zip(static, x):
+            t.copy_(src)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(i, j) for i, j in zip(w, out))
+    tlp.device_check()
+
+
+def test_explicit_stream_and_outputs():
+    g = torch.Generator(device="cuda").manual_seed(8)
+    q, k, v = (torch.randn(1, 70, 2, 32, generator=g, device="cuda").half() for _ in range(3))
+    o0, lse0 = tlp.attention_forward(q, k, v)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    o, lse = torch.empty_like(o0), torch.empty_like(lse0)
+    st.wait_stream(torch.cuda.current_stream())
+    r = tlp.attention_forward(q, k, v, o=o, lse=lse, stream=st)
+    st.synchronize()
+    assert r[0] is o and r[1] is lse and torch.equal(o, o0) and torch.equal(lse, lse0)
+
+
+def test_python_refusals():
+    q = torch.zeros(2, 16, 2, 64, device="cuda", dtype=torch.bfloat16)
+    lse = torch.zeros(2, 2, 16, device="cuda")
+    table = torch.zeros(32, 2, device="cuda", dtype=torch.bfloat16)
+    bad = [
+        lambda: tlp.attention_forward(q[0], q[0], q[0]),
+        lambda: tlp.attention_forward(q, q[:, :8], q),
+        lambda: tlp.attention_forward(q, q, q.half()),
+        lambda: tlp.attention_forward(q, q, q.cpu()),
+        lambda: tlp.attention_forward(q, q, q, o=q),
+        lambda: tlp.attention_forward(q, q, q, scale=0.0),
+        lambda: tlp.attention_forward(q, q, q, scale=-1.0),
+        lambda: tlp.attention_forward(q, q, q, mask=torch.zeros(2, 15, device="cuda")),
+        lambda: tlp.attention_forward(q, q, q, mask=torch.zeros(2, 16, device="cuda", dtype=torch.bool)),
+        lambda: tlp.attention_forward(q, q, q, mask=torch.zeros(2, 1, device="cuda").expand(2, 16)),
+        lambda: tlp.attention_forward(q, q, q, bias_table=table.float()),
+        lambda: tlp.attention_forward(q, q, q, bias_table=table[:, :1]),
+        lambda: tlp.attention_forward(q, q, q, bias_table=table, max_distance=8),
+        lambda: tlp.attention_forward(q, q, q, bias_table=table[:31]),
+        lambda: tlp.attention_forward(q, q, q, lse=lse[:1]),
+        lambda: tlp.attention_forward(q[..., :60], q[..., :60], q[..., :60]),
+        lambda: tlp.attention_forward(q[..., 1:57], q[..., 1:57], q[..., 1:57]),
+        lambda: tlp.attention_forward(q[:, :, :, ::2], q[:, :, :, ::2], q[:, :, :, ::2]),
+        lambda: tlp.attention_forward(q, q[:, :1].expand(2, 16, 2, 64), q),
+        lambda: tlp.attention_forward(q[:, :0], q[:, :0], q[:, :0]),
+        lambda: tlp.attention_backward(q, q, q, q, lse.half(), q),
+        lambda: tlp.attention_backward(q, q, q, q, lse, q, dtable=torch.zeros(32, 2, device="cuda")),
+        lambda: tlp.attention_backward(q, q, q, q, lse, q, bias_table=table, accumulate=True),
+        lambda: tlp.attention_backward(q, q, q, q, lse, q, dq=q),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises(tlp.TlError):
+            f()
+            pytest.fail(f"call {i} was taken")
+    tlp.device_check()

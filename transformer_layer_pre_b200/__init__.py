@@ -16,7 +16,8 @@ import torch
 __all__ = ["Layer", "Options", "TlError", "LibraryMissing", "load_library", "dropout_keep_mask",
            "WEIGHT_NAMES", "DTYPE_CODES", "EXPORTED_SYMBOLS", "device_check",
            "profile_enable", "profile_read", "launch_count", "PROFILE_CLASSES",
-           "pld_theta", "pld_keep_prob", "pld_keep", "set_wait_limit", "wait_probe"]
+           "pld_theta", "pld_keep_prob", "pld_keep", "set_wait_limit", "wait_probe",
+           "attention_forward", "attention_backward", "clip_grad_norm"]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libtlp.so")
@@ -33,6 +34,8 @@ EXPORTED_SYMBOLS = (
     "tl_profile_read", "tl_launch_count", "tl_bias_grad_noalloc", "tl_gelu_eval", "tl_status_string",
     "tl_pld_theta", "tl_pld_keep_prob", "tl_pld_keep", "tl_gelu_tanh_eval",
     "tl_set_wait_limit_ns", "tl_wait_probe", "layer_scratch_bytes", "layer_share_scratch",
+    "tl_attention_workspace_bytes", "tl_attention_forward", "tl_attention_backward",
+    "tl_clip_workspace_bytes", "tl_clip_grad_norm",
 )
 PROFILE_CLASSES = ("gemm", "attn_fwd", "attn_bwd", "ln_fwd", "ln_bwd", "rowwise")
 
@@ -59,6 +62,17 @@ class Options(ctypes.Structure):
         ("gelu_tanh", ctypes.c_int),
         ("stochastic_mode", ctypes.c_int),
     ]
+
+
+class _Attention(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("batch", ctypes.c_int), ("seq", ctypes.c_int), ("heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("scale", ctypes.c_float), ("mask", ctypes.c_void_p),
+                ("bias_table", ctypes.c_void_p), ("buckets", ctypes.c_int), ("max_distance", ctypes.c_int)]
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch", ctypes.c_int64), ("token", ctypes.c_int64),
+                ("head", ctypes.c_int64)]
 
 
 class _Weights(ctypes.Structure):
@@ -130,6 +144,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.tl_set_wait_limit_ns.restype = i
     lib.tl_wait_probe.argtypes = [vp]
     lib.tl_wait_probe.restype = i
+    sz, desc, heads = ctypes.c_size_t, ctypes.POINTER(_Attention), ctypes.POINTER(_Heads)
+    lib.tl_attention_workspace_bytes.argtypes = [desc, i]
+    lib.tl_attention_workspace_bytes.restype = sz
+    lib.tl_attention_forward.argtypes = [desc] + [heads] * 4 + [vp, vp, sz, vp]
+    lib.tl_attention_forward.restype = i
+    lib.tl_attention_backward.argtypes = [desc] + [heads] * 5 + [vp] + [heads] * 3 + [vp, i, vp, sz, vp]
+    lib.tl_attention_backward.restype = i
+    lib.tl_clip_workspace_bytes.argtypes = [i]
+    lib.tl_clip_workspace_bytes.restype = sz
+    lib.tl_clip_grad_norm.argtypes = [i, i, vp, vp, vp, f, vp, vp, sz, vp]
+    lib.tl_clip_grad_norm.restype = i
     _lib = lib
     return lib
 
@@ -242,6 +267,157 @@ class Layer:
             self.close()
         except Exception:
             pass
+
+
+def _fail(what: str):
+    raise TlError(1, what)
+
+
+def _on(device, stream):
+    """The stream a call is enqueued on: the current one of the tensors'
+    device, or the given one, which must be of that device."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if stream.device != device:
+        _fail(f"a stream of {stream.device} for tensors on {device}")
+    return stream
+
+
+def _attention_call(q, k, v, mask, bias_table, max_distance, scale, others, lse):
+    """Checks shared by both attention calls; returns the description."""
+    if q.dim() != 4 or not q.is_cuda or q.dtype not in DTYPE_CODES:
+        _fail("q must be a (batch, seq, heads, head_dim) float32, float16 or bfloat16 tensor on a CUDA device")
+    device, dtype, shape = q.device, q.dtype, q.shape
+    for name, t in (("k", k), ("v", v), *others):
+        if t.shape != shape or t.dtype != dtype or t.device != device:
+            _fail(f"{name} must have q's shape, dtype and device")
+    b, s, n, d = shape
+    for name, t in (("q", q), ("k", k), ("v", v), *others):
+        if d > 1 and t.stride(3) != 1:
+            _fail(f"the head_dim entries of {name} must be contiguous")
+    desc = _Attention(DTYPE_CODES[dtype], b, s, n, d, 0.0 if scale is None else scale, None, None, 0, 0)
+    if scale is not None and not scale > 0.0:
+        _fail("scale must be positive")
+    if mask is not None:
+        if mask.shape != (b, s) or mask.dtype != torch.float32 or mask.device != device or not mask.is_contiguous():
+            _fail("mask must be a contiguous (batch, seq) float32 tensor on q's device")
+        desc.mask = mask.data_ptr()
+    if bias_table is not None:
+        if (bias_table.dim() != 2 or bias_table.shape[1] != n or bias_table.dtype != dtype
+                or bias_table.device != device or not bias_table.is_contiguous()):
+            _fail("bias_table must be a contiguous (buckets, heads) tensor of q's dtype on q's device")
+        desc.bias_table = bias_table.data_ptr()
+        desc.buckets = bias_table.shape[0]
+        desc.max_distance = max_distance
+    if lse is not None and (lse.shape != (b, n, s) or lse.dtype != torch.float32 or lse.device != device
+                            or not lse.is_contiguous()):
+        _fail("lse must be a contiguous (batch, heads, seq) float32 tensor on q's device")
+    return desc
+
+
+def _heads(t):
+    sb, st, sh, _ = t.stride()
+    return _Heads(t.data_ptr(), sb, st, sh)
+
+
+def _workspace(lib, desc, backward, stream, device):
+    n = lib.tl_attention_workspace_bytes(ctypes.byref(desc), backward)
+    with torch.cuda.stream(stream):
+        return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def _run(fn, device, *args):
+    with torch.cuda.device(device):
+        st = fn(*args)
+    if st != 0:
+        raise TlError(st, load_library().tl_status_string(st).decode())
+
+
+def attention_forward(q, k, v, mask=None, bias_table=None, max_distance=128, scale=None, o=None, lse=None,
+                      stream=None):
+    """softmax(scale q k^T + bias + mask) v for every sequence and head, with
+    an optional learned relative position bias.
+
+    q, k, v: (batch, seq, heads, head_dim), head_dim contiguous, any other
+    strides that are multiples of 16 bytes (views of a packed projection, for
+    instance).  mask: (batch, seq) float32, added over the keys (-1e30 or less
+    removes the key).  bias_table: (buckets, heads) of q's dtype; the bias of
+    query i and key j is its entry for bucket(j - i) (include/tlp.h).  scale:
+    default 1/sqrt(head_dim).  Returns (o, lse): o like q (dense unless
+    given), lse (batch, heads, seq) float32, which the backward needs."""
+    lib = load_library()
+    desc = _attention_call(q, k, v, mask, bias_table, max_distance, scale, (("o", o),) if o is not None else (), lse)
+    stream = _on(q.device, stream)
+    with torch.cuda.stream(stream):
+        if o is None:
+            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if lse is None:
+            lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32, device=q.device)
+    ws = _workspace(lib, desc, 0, stream, q.device)
+    _run(lib.tl_attention_forward, q.device, desc, _heads(q), _heads(k), _heads(v), _heads(o), lse.data_ptr(),
+         ws.data_ptr(), ws.numel(), stream.cuda_stream)
+    return o, lse
+
+
+def attention_backward(q, k, v, o, lse, do, mask=None, bias_table=None, max_distance=128, scale=None, dq=None,
+                       dk=None, dv=None, dtable=None, accumulate=False, stream=None):
+    """Gradients of attention_forward from its inputs, its o and lse, and do,
+    the gradient of o: (dq, dk, dv, dtable).  The probabilities are recomputed
+    from lse.  dq, dk, dv are written (dense unless given); dtable, (buckets,
+    heads) float32, is None without a bias_table, and added to when it is
+    given with accumulate=True (a table shared by several layers)."""
+    lib = load_library()
+    outs = [(n, t) for n, t in (("dq", dq), ("dk", dk), ("dv", dv)) if t is not None]
+    desc = _attention_call(q, k, v, mask, bias_table, max_distance, scale, (("o", o), ("do", do), *outs), lse)
+    if dtable is not None and (bias_table is None or dtable.shape != bias_table.shape or dtable.dtype != torch.float32
+                               or dtable.device != q.device or not dtable.is_contiguous()):
+        _fail("dtable must be a contiguous float32 tensor of bias_table's shape on q's device")
+    if accumulate and dtable is None:
+        _fail("accumulate needs the dtable to add to")
+    stream = _on(q.device, stream)
+    with torch.cuda.stream(stream):
+        dq, dk, dv = (torch.empty(q.shape, dtype=q.dtype, device=q.device) if t is None else t for t in (dq, dk, dv))
+        if dtable is None and bias_table is not None:
+            dtable = torch.empty(bias_table.shape, dtype=torch.float32, device=q.device)
+    ws = _workspace(lib, desc, 1, stream, q.device)
+    _run(lib.tl_attention_backward, q.device, desc, _heads(q), _heads(k), _heads(v), _heads(o), _heads(do),
+         lse.data_ptr(), _heads(dq), _heads(dk), _heads(dv), _ptr(dtable), int(accumulate), ws.data_ptr(),
+         ws.numel(), stream.cuda_stream)
+    return dq, dk, dv, dtable
+
+
+def clip_grad_norm(grads, max_norm, out=None, stream=None):
+    """Scales gradients so that their global 2-norm is at most max_norm:
+    g * min(1, max_norm / (norm + 1e-6)).  grads: dense tensors of one dtype
+    (float32, float16 or bfloat16) and device; scaled in place, or written to
+    the tensors of `out` (same sizes and dtype).  Returns the norm before
+    clipping, a (1,) float32 tensor on the device: no host synchronisation."""
+    lib = load_library()
+    grads = list(grads)
+    outs = grads if out is None else list(out)
+    if not grads or len(outs) != len(grads):
+        _fail("a non-empty list of gradients, and as many outputs")
+    device, dtype = grads[0].device, grads[0].dtype
+    if device.type != "cuda" or dtype not in DTYPE_CODES:
+        _fail("gradients must be float32, float16 or bfloat16 tensors on a CUDA device")
+    for t in grads if out is None else grads + outs:
+        if t.dtype != dtype or t.device != device or not t.is_contiguous():
+            _fail("gradients and outputs must be contiguous tensors of one dtype and device")
+    n = len(grads)
+    sizes = [t.numel() for t in grads]
+    src = (ctypes.c_void_p * n)(*[t.data_ptr() for t in grads])
+    dst = src
+    if out is not None:
+        if [t.numel() for t in outs] != sizes:
+            _fail("an output for every gradient, of its size")
+        dst = (ctypes.c_void_p * n)(*[t.data_ptr() for t in outs])
+    stream = _on(device, stream)
+    with torch.cuda.stream(stream):
+        norm = torch.empty(1, dtype=torch.float32, device=device)
+        ws = torch.empty(lib.tl_clip_workspace_bytes(n), dtype=torch.uint8, device=device)
+    _run(lib.tl_clip_grad_norm, device, DTYPE_CODES[dtype], n, src, dst, (ctypes.c_uint64 * n)(*sizes), max_norm,
+         norm.data_ptr(), ws.data_ptr(), ws.numel(), stream.cuda_stream)
+    return norm
 
 
 def device_check() -> None:

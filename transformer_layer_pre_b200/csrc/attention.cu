@@ -1,0 +1,350 @@
+// attention.cu — the attention entry points: argument checks, the workspace,
+// the launch that prepares it, and the sum of the bias table's gradient.
+#include <math.h>
+#include <string.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/tlp.h"
+#include "attention.cuh"
+#include "kernels.h"
+#include "profile.h"
+
+namespace tlp {
+namespace {
+
+constexpr int kPrepThreads = 256;
+
+// One launch fills the workspace (layout at the top of attention.cuh).
+// Blocks [0, nmask): 256 keys each of maskx and flags.  Then nvec blocks: 256
+// diagonals of one head each, written to every copy.  Then (backward) blocks
+// of 256 / G rows for stats, G lanes per row reading 16 bytes each; rows run
+// (b, token, head) with the head fastest, the order in which O and dO lie in
+// (B, S, heads, d) memory.
+// Bound: HBM in the backward (reads O and dO once), launch latency otherwise.
+template <typename T, int G>
+__global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(const __grid_constant__ AttnOp a, int nmask, int nvec) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tid = threadIdx.x;
+  int blk = blockIdx.x;
+  if (blk < nmask) {
+    __shared__ int any[kPrepThreads / kAttnFlagKeys], zero[kPrepThreads / kAttnFlagKeys];
+    const int per = (a.Sp + kPrepThreads - 1) / kPrepThreads;
+    const int b = blk / per, j = (blk - b * per) * kPrepThreads + tid;
+    const int g = tid / kAttnFlagKeys;
+    if (tid < kPrepThreads / kAttnFlagKeys) any[tid] = 0, zero[tid] = 1;
+    __syncthreads();
+    if (j < a.Sp) {
+      float v = -INFINITY;
+      if (j < a.S) {
+        const float m = a.mask ? a.mask[(size_t)b * a.S + j] : 0.0f;
+        v = m <= kAttnMasked ? -INFINITY : m * kAttnLog2e;
+      }
+      a.maskx[(size_t)b * a.Sp + j] = v;
+      if (v != -INFINITY) any[g] = 1;
+      if (v != 0.0f) zero[g] = 0;
+    }
+    __syncthreads();
+    if (j < a.Sp && tid % kAttnFlagKeys == 0)
+      a.flags[b * (a.Sp / kAttnFlagKeys) + j / kAttnFlagKeys] = zero[g] ? 0 : (any[g] ? 1 : 2);
+    return;
+  }
+  blk -= nmask;
+  if (blk < nvec) {
+    const int per = (a.vec_len + kPrepThreads - 1) / kPrepThreads;
+    const int h = blk / per, X = (blk - h * per) * kPrepThreads + tid;
+    if (X >= a.vec_len) return;
+    const int x = max(-a.sat, min(a.sat, X - a.vec_off));   // key minus query
+    float v = 0.0f;
+    for (int u = 0; u < a.buckets; ++u)
+      if (x >= a.lo[u] && x - a.lo[u] < a.n[u]) {
+        v = to_f(static_cast<const T*>(a.table)[(size_t)u * a.nh + h]) * kAttnLog2e;
+        break;
+      }
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      float* base = a.vec + ((size_t)h * 8 + s) * a.vec_len;
+      if (X - s >= 0) base[X - s] = v;
+      // direction 1: diagonal -x, at index -x + vec_off
+      const int Y = 2 * a.vec_off - X - s;
+      if (Y >= 0 && Y < a.vec_len) base[(size_t)4 * a.vec_len + Y] = v;
+    }
+    return;
+  }
+  blk -= nvec;
+  constexpr int kEl = 16 / sizeof(T);
+  const long long row = (long long)blk * (kPrepThreads / G) + tid / G;
+  const long long rows = (long long)a.B * a.Sp * a.nh;
+  const int lane = tid % G;
+  float t = 0.0f;
+  int b = 0, i = 0, h = 0;
+  if (row < rows) {
+    h = (int)(row % a.nh);
+    i = (int)(row / a.nh % a.Sp);
+    b = (int)(row / a.nh / a.Sp);
+    if (i < a.S)
+      for (int c = lane * kEl; c < a.d; c += G * kEl) {
+        const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.o.p) + (size_t)b * a.o.sb +
+                                                        (size_t)i * a.o.st + (size_t)h * a.o.sh + c);
+        const uint4 y = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.dout.p) + (size_t)b * a.dout.sb +
+                                                        (size_t)i * a.dout.st + (size_t)h * a.dout.sh + c);
+        const T *xe = reinterpret_cast<const T*>(&x), *ye = reinterpret_cast<const T*>(&y);
+#pragma unroll
+        for (int k = 0; k < kEl; ++k) t = fmaf(to_f(xe[k]), to_f(ye[k]), t);
+      }
+  }
+#pragma unroll
+  for (int w = G / 2; w > 0; w >>= 1) t += __shfl_xor_sync(0xffffffffu, t, w);
+  if (row < rows && lane == 0) {
+    const size_t bh = (size_t)b * a.nh + h;
+    float* st = a.stats + bh * 2 * a.Sp;
+    st[i] = i < a.S ? a.lse[bh * a.S + i] * kAttnLog2e : INFINITY;
+    st[a.Sp + i] = i < a.S ? t : 0.0f;
+  }
+}
+
+// dtable[u, h] (+)= sum over sequences and items of dpart, in a fixed order:
+// one warp per (bucket, head), float64 across the partials.
+__global__ void __launch_bounds__(256) attn_table_grad_kernel(const __grid_constant__ AttnOp a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int w = (blockIdx.x * 256 + threadIdx.x) >> 5, lane = threadIdx.x & 31;
+  if (w >= a.buckets * a.nh) return;
+  const int u = w / a.nh, h = w - u * a.nh;
+  const int rows = a.B * a.ditems;
+  double t = 0.0;
+  for (int r = lane; r < rows; r += 32) {
+    const int b = r / a.ditems, it = r - b * a.ditems;
+    t += (double)a.dpart[(((size_t)b * a.nh + h) * a.ditems + it) * a.buckets + u];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  if (lane == 0) {
+    float* d = a.dtable + (size_t)u * a.nh + h;
+    *d = (float)(a.daccumulate ? (double)*d + t : t);
+  }
+}
+
+template <typename T, int G>
+void prep(const AttnOp& a, bool backward, cudaStream_t s) {
+  const int nmask = a.mask_seqs * ((a.Sp + kPrepThreads - 1) / kPrepThreads);
+  const int nvec = a.vec ? a.nh * ((a.vec_len + kPrepThreads - 1) / kPrepThreads) : 0;
+  const long long rows = backward ? (long long)a.B * a.Sp * a.nh : 0;
+  const int nrow = (int)((rows + kPrepThreads / G - 1) / (kPrepThreads / G));
+  launch_pdl(attn_prep_kernel<T, G>, nmask + nvec + nrow, kPrepThreads, 0, s, a, nmask, nvec);
+  count_launch();
+}
+
+template <typename T>
+void prep_t(const AttnOp& a, bool backward, cudaStream_t s) {
+  // lanes per row of the D = rowsum(dO O) part: 16 bytes each
+  const int vecs = a.d * (int)sizeof(T) / 16;
+  if (vecs <= 4) prep<T, 4>(a, backward, s);
+  else if (vecs <= 8) prep<T, 8>(a, backward, s);
+  else prep<T, 16>(a, backward, s);
+}
+
+// Bucket of a key n >= 0 positions behind the query (half = buckets of a side).
+int side_bucket(long long n, int half, int max_distance) {
+  const int first = half / 2;
+  if (n < first) return (int)n;
+  const double f = std::log((double)n / first) / std::log((double)max_distance / first) * (half - first) + 1e-9;
+  return first + (int)std::min((double)(half - first - 1), std::floor(f));
+}
+
+// The diagonals of every bucket, and the distance from which on the last one holds.
+void bucket_ranges(AttnOp& a, int max_distance) {
+  const int half = a.buckets / 2, first = half / 2;
+  constexpr int kFar = 1 << 30;
+  int from[kAttnMaxBuckets / 2 + 1];   // smallest distance of each bucket of a side
+  for (int u = 0; u < half; ++u) {
+    if (u <= first) {
+      from[u] = u;
+      continue;
+    }
+    long long n = (long long)std::ceil(first * std::pow((double)max_distance / first, (double)(u - first) / (half - first)));
+    n = std::max<long long>(n, first);
+    while (n > first && side_bucket(n - 1, half, max_distance) >= u) --n;
+    while (side_bucket(n, half, max_distance) < u) ++n;
+    from[u] = (int)n;
+  }
+  from[half] = kFar;
+  for (int u = 0; u < half; ++u) {
+    // keys at or behind the query: diagonals -(from[u+1] - 1) .. -from[u]
+    a.n[u] = std::max(0, from[u + 1] - from[u]);
+    a.lo[u] = -(from[u + 1] - 1);
+    // keys ahead: the same distances, without 0
+    const int f = std::max(1, from[u]);
+    a.n[half + u] = std::max(0, from[u + 1] - f);
+    a.lo[half + u] = f;
+  }
+  a.sat = std::max(1, from[half - 1]);
+}
+
+bool view_ok(const tl_heads* v, int dt, int B, int S, int nh, int d) {
+  if (!v || !v->data) return false;
+  const int64_t per = dt == DT_F32 ? 4 : 8;   // elements in 16 bytes
+  if (reinterpret_cast<uintptr_t>(v->data) & 15) return false;
+  const int64_t st[3] = {v->batch, v->token, v->head};
+  const int n[3] = {B, S, nh};
+  for (int i = 0; i < 3; ++i)
+    if (n[i] > 1 && (st[i] < d || st[i] % per != 0 || st[i] >= (1ll << 36))) return false;
+  return true;
+}
+
+// Strides of dimensions of one entry mean nothing and may hold anything.
+AttnView view(const tl_heads* v, int B, int S, int nh, int d) {
+  AttnView w;
+  w.p = v->data;
+  w.sb = B > 1 ? v->batch : (d + 7) / 8 * 8;
+  w.st = S > 1 ? v->token : (d + 7) / 8 * 8;
+  w.sh = nh > 1 ? v->head : (d + 7) / 8 * 8;
+  return w;
+}
+
+size_t take(size_t& off, size_t bytes) {
+  const size_t at = off;
+  off += (bytes + 255) & ~(size_t)255;
+  return at;
+}
+
+// Checks what does not depend on the tensors and lays out the workspace
+// (base null: measures).
+tl_status plan(const tl_attention* c, bool backward, char* base, AttnOp& a, size_t& bytes) {
+  memset(&a, 0, sizeof(a));
+  if (!c || c->dtype < TL_F32 || c->dtype > TL_BF16) return TL_EINVAL;
+  if (c->batch <= 0 || c->seq <= 0 || c->heads <= 0) return TL_EINVAL;
+  if (c->head_dim <= 0 || c->head_dim > 128 || c->head_dim % 8 != 0) return TL_EINVAL;
+  if (!(c->scale >= 0.0f) || isinf(c->scale)) return TL_EINVAL;
+  if (reinterpret_cast<uintptr_t>(c->mask) & 3) return TL_EINVAL;
+  if (c->bias_table) {
+    if (c->buckets < 4 || c->buckets > kAttnMaxBuckets || c->buckets % 2 != 0) return TL_EINVAL;
+    if (c->max_distance <= c->buckets / 4 || c->max_distance > (1 << 20)) return TL_EINVAL;
+    if (reinterpret_cast<uintptr_t>(c->bias_table) & (dtype_size(c->dtype) - 1)) return TL_EINVAL;
+  }
+  if (c->seq > (1 << 20) || (long long)c->batch * c->heads * ((c->seq + 127) / 128 * 128) > (1ll << 30))
+    return TL_EUNSUPPORTED;
+  a.B = c->batch; a.S = c->seq; a.nh = c->heads; a.d = c->head_dim;
+  a.Sp = (a.S + 127) / 128 * 128;
+  a.scale = c->scale > 0.0f ? c->scale : (float)(1.0 / std::sqrt((double)a.d));
+  a.c2 = a.scale * kAttnLog2e;
+  a.mask = c->mask;
+  a.mask_seqs = c->mask ? a.B : 1;
+  size_t off = 0;
+  a.maskx = (float*)(base + take(off, (size_t)a.mask_seqs * a.Sp * 4));
+  a.flags = (int*)(base + take(off, (size_t)a.mask_seqs * (a.Sp / kAttnFlagKeys) * 4));
+  if (c->bias_table) {
+    a.table = c->bias_table;
+    a.buckets = c->buckets;
+    bucket_ranges(a, c->max_distance);
+    // no diagonal beyond the sequence is read: windows of 256 diagonals start
+    // up to 128 before and end up to 256 after the last one that matters
+    const int reach = std::min(a.sat, a.Sp);
+    a.vec_off = (reach + 127) / 128 * 128 + 384;
+    a.vec_len = 2 * a.vec_off + 128;
+    a.sat = reach;
+    a.vec = (float*)(base + take(off, (size_t)a.nh * 8 * a.vec_len * 4));
+  }
+  if (backward) {
+    a.stats = (float*)(base + take(off, (size_t)a.B * a.nh * 2 * a.Sp * 4));
+    if (c->bias_table) {
+      a.ditems = (a.S + 63) / 64;   // rows of 64 queries at most
+      a.dpart = (float*)(base + take(off, (size_t)a.B * a.nh * a.ditems * a.buckets * 4));
+    }
+  }
+  bytes = off;
+  return TL_OK;
+}
+
+bool same(const tl_heads* x, const tl_heads* y) { return x->data == y->data; }
+
+}  // namespace
+
+void attn_prep_run(int dt, const AttnOp& a, bool backward, cudaStream_t s) {
+  if (dt == DT_F32) prep_t<float>(a, backward, s);
+  else if (dt == DT_F16) prep_t<half_t>(a, backward, s);
+  else prep_t<bf16_t>(a, backward, s);
+}
+
+void attn_table_grad_run(const AttnOp& a, cudaStream_t s) {
+  launch_pdl(attn_table_grad_kernel, (a.buckets * a.nh + 7) / 8, 256, 0, s, a);
+  count_launch();
+}
+
+}  // namespace tlp
+
+using namespace tlp;
+
+extern "C" {
+
+size_t tl_attention_workspace_bytes(const tl_attention* c, int backward) {
+  AttnOp a;
+  size_t bytes = 0;
+  return plan(c, backward != 0, nullptr, a, bytes) == TL_OK ? bytes : 0;
+}
+
+tl_status tl_attention_forward(const tl_attention* c, const tl_heads* q, const tl_heads* k, const tl_heads* v,
+                               const tl_heads* o, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  AttnOp a;
+  size_t need = 0;
+  const tl_status st = plan(c, false, (char*)workspace, a, need);
+  if (st != TL_OK) return st;
+  const tl_heads* all[4] = {q, k, v, o};
+  for (const tl_heads* t : all)
+    if (!view_ok(t, c->dtype, a.B, a.S, a.nh, a.d)) return TL_EINVAL;
+  if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3) || same(o, q) || same(o, k) || same(o, v)) return TL_EINVAL;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < need) return TL_EINVAL;
+  if (cudaGetLastError() != cudaSuccess) return TL_ECUDA;
+  a.q = view(q, a.B, a.S, a.nh, a.d);
+  a.k = view(k, a.B, a.S, a.nh, a.d);
+  a.v = view(v, a.B, a.S, a.nh, a.d);
+  a.o = view(o, a.B, a.S, a.nh, a.d);
+  a.lse = lse;
+  cudaStream_t s = (cudaStream_t)stream;
+  ProfScope p_(PC_ATTN_FWD, s);
+  attn_prep_run(c->dtype, a, false, s);
+  attn_simt_op_fwd_run(c->dtype, a, s);
+  return cudaGetLastError() == cudaSuccess ? TL_OK : TL_ECUDA;
+}
+
+tl_status tl_attention_backward(const tl_attention* c, const tl_heads* q, const tl_heads* k, const tl_heads* v,
+                                const tl_heads* o, const tl_heads* dout, const float* lse, const tl_heads* dq,
+                                const tl_heads* dk, const tl_heads* dv, float* dtable, int accumulate, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  AttnOp a;
+  size_t need = 0;
+  const tl_status st = plan(c, true, (char*)workspace, a, need);
+  if (st != TL_OK) return st;
+  const tl_heads* all[8] = {q, k, v, o, dout, dq, dk, dv};
+  for (const tl_heads* t : all)
+    if (!view_ok(t, c->dtype, a.B, a.S, a.nh, a.d)) return TL_EINVAL;
+  for (int i = 5; i < 8; ++i)
+    for (int j = 0; j < i; ++j)
+      if (same(all[i], all[j])) return TL_EINVAL;
+  if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3)) return TL_EINVAL;
+  if (dtable && (!c->bias_table || (reinterpret_cast<uintptr_t>(dtable) & 3))) return TL_EINVAL;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < need) return TL_EINVAL;
+  if (cudaGetLastError() != cudaSuccess) return TL_ECUDA;
+  a.q = view(q, a.B, a.S, a.nh, a.d);
+  a.k = view(k, a.B, a.S, a.nh, a.d);
+  a.v = view(v, a.B, a.S, a.nh, a.d);
+  a.o = view(o, a.B, a.S, a.nh, a.d);
+  a.dout = view(dout, a.B, a.S, a.nh, a.d);
+  a.dq = view(dq, a.B, a.S, a.nh, a.d);
+  a.dk = view(dk, a.B, a.S, a.nh, a.d);
+  a.dv = view(dv, a.B, a.S, a.nh, a.d);
+  a.lse = const_cast<float*>(lse);
+  a.dtable = dtable;
+  a.daccumulate = accumulate ? 1 : 0;
+  if (!dtable) a.dpart = nullptr;
+  cudaStream_t s = (cudaStream_t)stream;
+  ProfScope p_(PC_ATTN_BWD, s);
+  attn_prep_run(c->dtype, a, true, s);
+  attn_simt_op_bwd_run(c->dtype, a, s);
+  if (dtable) attn_table_grad_run(a, s);
+  return cudaGetLastError() == cudaSuccess ? TL_OK : TL_ECUDA;
+}
+
+}  // extern "C"

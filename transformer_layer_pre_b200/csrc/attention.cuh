@@ -1,0 +1,76 @@
+// attention.cuh — what the kernels of the attention entry points
+// (tl_attention_forward, tl_attention_backward) share: the launch arguments
+// and the layout of the prepared workspace.
+//
+// Per sequence b and head h (c = scale, T the bias table):
+//   x_ij = log2(e) (c q_i.k_j + T[bucket(j - i), h] + mask_bj)
+//   P_ij = 2^(x_ij - lse2_i), lse2_i = log2 sum_j 2^x_ij
+// Everything added to q_i.k_j is prepared in log2 units by one launch
+// (attn_prep_kernel) into the workspace:
+//   maskx  [B or 1][Sp]      log2(e) * mask, -inf for a removed key and past the sequence end
+//   flags  [B or 1][Sp / 64] of each 64 keys: 0 all of maskx is 0, 1 mixed, 2 every key removed
+//   vec    [heads][dirs][4][len] the bias along the diagonals, see bias_at
+//   stats  [B * heads][2][Sp] backward: lse2 (+inf for an empty row and past the end), D = dO.O
+// with Sp = the sequence length rounded up to 128.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace tlp {
+
+constexpr float kAttnLog2e = 1.4426950408889634f;
+constexpr float kAttnLn2 = 0.6931471805599453f;
+constexpr float kAttnMasked = -1e30f;      // a mask value at or below this removes the key
+constexpr int kAttnMaxBuckets = 256;
+constexpr int kAttnFlagKeys = 64;
+
+// A (batch, token, head, dim) tensor: element strides, dim contiguous.
+struct AttnView {
+  void* p;
+  long long sb, st, sh;
+};
+
+struct AttnOp {
+  int B, S, Sp, nh, d;
+  float scale;               // c
+  float c2;                  // c * log2(e)
+  AttnView q, k, v, o, dout, dq, dk, dv;
+  float* lse;                // (B, nh, S)
+  // prepared inputs
+  const float* mask;         // (B, S) or null
+  const void* table;         // (buckets, nh) or null
+  int buckets;
+  float* maskx;
+  int* flags;
+  int mask_seqs;             // B, or 1 without a mask (every sequence reads row 0)
+  float* vec;                // null without a table
+  int vec_len, vec_off;      // floats per copy; offset of diagonal 0
+  int sat;                   // |j - i| >= sat: the bias no longer depends on the distance
+  float* stats;
+  // bias table gradient: partial sums [B * nh][items][buckets], null when not wanted
+  float* dpart;
+  int ditems;                // partial rows per (b, h)
+  float* dtable;             // (buckets, nh)
+  int daccumulate;
+  // bucket u holds the diagonals j - i in [lo[u], lo[u] + n[u]) (n = 0: none)
+  int lo[kAttnMaxBuckets], n[kAttnMaxBuckets];
+  int* err;
+};
+
+// The bias of diagonal x = j - i (direction 0) or x = i - j (direction 1), in
+// log2 units: copy s of a direction holds the diagonal x at index
+// x + vec_off - s, so a run that starts at any x begins 16-byte aligned in
+// one of the four copies.
+__device__ __forceinline__ const float* bias_copy(const AttnOp& a, int h, int dir, int s) {
+  return a.vec + ((size_t)(h * 2 + dir) * 4 + s) * a.vec_len;
+}
+
+void attn_prep_run(int dt, const AttnOp& a, bool backward, cudaStream_t s);
+void attn_table_grad_run(const AttnOp& a, cudaStream_t s);
+void attn_simt_op_fwd_run(int dt, const AttnOp& a, cudaStream_t s);
+void attn_simt_op_bwd_run(int dt, const AttnOp& a, cudaStream_t s);
+
+}  // namespace tlp
