@@ -305,8 +305,10 @@ tl_status tl_attention_forward(const tl_attention* c, const tl_heads* q, const t
   cudaStream_t s = (cudaStream_t)stream;
   ProfScope p_(PC_ATTN_FWD, s);
   attn_prep_run(c->dtype, a, false, s);
-  attn_simt_op_fwd_run(c->dtype, a, s);
-  return cudaGetLastError() == cudaSuccess ? TL_OK : TL_ECUDA;
+  bool ok = true;
+  if (c->dtype == TL_F32) attn_simt_op_fwd_run(c->dtype, a, s);
+  else ok = attention_tc_fwd_run(c->dtype, a, s);
+  return ok && cudaGetLastError() == cudaSuccess ? TL_OK : TL_ECUDA;
 }
 
 tl_status tl_attention_backward(const tl_attention* c, const tl_heads* q, const tl_heads* k, const tl_heads* v,

@@ -72,5 +72,7 @@ void attn_prep_run(int dt, const AttnOp& a, bool backward, cudaStream_t s);
 void attn_table_grad_run(const AttnOp& a, cudaStream_t s);
 void attn_simt_op_fwd_run(int dt, const AttnOp& a, cudaStream_t s);
 void attn_simt_op_bwd_run(int dt, const AttnOp& a, cudaStream_t s);
+// 16-bit storage; false when a tensor could not be described to the TMA unit
+bool attention_tc_fwd_run(int dt, const AttnOp& a, cudaStream_t s);
 
 }  // namespace tlp

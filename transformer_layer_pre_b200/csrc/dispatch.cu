@@ -40,18 +40,22 @@ int rowwise_take_error();
 void gemm_tc_set_wait_limit(uint64_t ns);
 void attn_tc_set_wait_limit(uint64_t ns);
 void rowwise_set_wait_limit(uint64_t ns);
+int attention_tc_take_error();
+void attention_tc_set_wait_limit(uint64_t ns);
 
 void device_set_wait_limit(uint64_t ns) {
   gemm_tc_set_wait_limit(ns);
   attn_tc_set_wait_limit(ns);
   rowwise_set_wait_limit(ns);
+  attention_tc_set_wait_limit(ns);
 }
 
 int device_take_error() {
   const int g = gemm_tc_take_error();
   const int a = attn_tc_take_error();
   const int r = rowwise_take_error();
-  return g ? g : (a ? a : r);
+  const int o = attention_tc_take_error();
+  return g ? g : (a ? a : (r ? r : o));
 }
 
 }  // namespace tlp

@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kClipThreads) clip_norm_kernel(const __grid_co
 #pragma unroll
     for (int u = 0; u < kClipUnroll; ++u) {
       const uint64_t i = threadIdx.x + u * kClipThreads;
-      r[u] = i < vecs ? __ldg(v + i) : make_uint4(0u, 0u, 0u, 0u);
+      r[u] = i < vecs ? v[i] : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
     for (int u = 0; u < kClipUnroll; ++u) acc += square_sum16<T>(r[u]);
