@@ -136,6 +136,8 @@ def test_long_many_items():
     _case("f16", 5, 130, 70, 64, mask="lengths")
     _case("bf16", 1, 3000, 2, 64, mask="lengths")
     _case("f16", 1, 2100, 1, 128)
+    _case("bf16", 5, 130, 70, 128, mask="lengths")
+    _case("f16", 3, 1100, 40, 96, mask="empty")
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])

@@ -54,10 +54,6 @@ template <> __device__ __forceinline__ uint32_t pack2<bf16_t>(float lo, float hi
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-__device__ __forceinline__ uint8_t* align1k(uint8_t* p) {
-  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
-}
-
 // 32 TMEM columns, no wait (the caller waits once for several).
 __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, float* r) {
   asm volatile(
@@ -170,14 +166,11 @@ struct LiveTiles {
 };
 
 // ============================================================================ forward
-// Two blocks of six warps per SM, each walking items (sequence, head, 128
-// queries) over 128-key tiles: while one block's softmax fills the
-// special-function units, the other's products fill the tensor cores.
-// Warps 0-3: softmax, one query row (TMEM lane) per thread; 4: TMA; 5: MMA.
-//
-// TMEM (256 columns a block).  D = 64: S 0-127, P 128-191, O 192-255, so
-// Q K^T of the next tile runs as soon as S is in registers.  D = 128: S 0-127
-// with P over its first half, O 128-255; the next Q K^T follows P V.
+// Blocks of six warps, four on an SM (D = 64; two for D = 128), each walking
+// items (sequence, head, 128 queries) over tiles of 64 (128) keys: while one
+// block's softmax fills the special-function units, the others' products and
+// loads are under way.  Warps 0-3: softmax, one query row (TMEM lane) per
+// thread; 4: TMA; 5: MMA.  TMEM: S, P over S once it is read, O.
 //
 // Online softmax with a lazy reference: P = 2^(x - ref), ref the row maximum
 // when O was last rescaled; O and the row sum are rescaled only once the
@@ -191,53 +184,59 @@ struct LiveTiles {
 // conflicts.
 template <int D>
 struct Fwd {
-  static constexpr int kTile = D / 64 * kRegion;
-  static constexpr int kQ = D == 64 ? 2 : 1;
+  static constexpr int kTK = D == 64 ? 64 : 128;                    // keys per tile
+  static constexpr int kBlocks = D == 64 ? 4 : 2;                   // per SM
+  static constexpr int kCols = D == 64 ? 128 : 256;                 // TMEM columns: S with P over it, O
+  static constexpr uint32_t kO = kTK;
+  static constexpr int kQBytes = D / 64 * kRegion;
+  static constexpr int kKvRegion = kTK * 128;
+  static constexpr int kKvBytes = D / 64 * kKvRegion;
   static constexpr int kKv = D == 64 ? 2 : 1;
   static constexpr int kAux = 2;
-  static constexpr int kWin = 264;                                  // floats of a window copy, 8 banks apart
-  static constexpr int kAuxBytes = 4 * kWin * 4 + 512 + 16;
-  static constexpr int kSmem = (kQ + 2 * kKv) * kTile + kAux * kAuxBytes + 256 + 1024;
-  static constexpr uint32_t kP = D == 64 ? 128 : 0;
-  static constexpr uint32_t kO = D == 64 ? 192 : 128;
+  static constexpr int kRun = kTK + 128;                            // diagonals of a tile, rounded up
+  static constexpr int kWin = kRun + 8;                             // floats of a window copy, 8 banks apart
+  static constexpr int kAuxBytes = 4 * kWin * 4 + kTK * 4 + 16;
+  static constexpr int kSmem = kQBytes + 2 * kKv * kKvBytes + kAux * kAuxBytes + 208;
 };
+static_assert(4 * (Fwd<64>::kSmem + 1024) <= 228 * 1024 && 2 * (Fwd<128>::kSmem + 1024) <= 228 * 1024,
+              "the blocks of an SM do not fit its shared memory");
 constexpr int kFwdThreads = 192;
 constexpr float kRescale = 8.0f;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kFwdThreads, 2)
+__global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
     attention_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                          const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
                          const __grid_constant__ AttnOp a) {
   using C = Fwd<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sQ = align1k(smem_raw);
-  uint8_t* sK = sQ + C::kQ * C::kTile;
-  uint8_t* sV = sK + C::kKv * C::kTile;
-  uint8_t* sAux = sV + C::kKv * C::kTile;
+  // the only shared memory of the kernel: its start is 1024-byte aligned
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sQ = smem_raw;
+  uint8_t* sK = sQ + C::kQBytes;
+  uint8_t* sV = sK + C::kKv * C::kKvBytes;
+  uint8_t* sAux = sV + C::kKv * C::kKvBytes;
   uint64_t* bar = reinterpret_cast<uint64_t*>(sAux + C::kAux * C::kAuxBytes);
-  uint64_t *q_full = bar, *q_empty = q_full + C::kQ, *k_full = q_empty + C::kQ, *k_empty = k_full + C::kKv,
+  uint64_t *q_full = bar, *q_empty = q_full + 1, *k_full = q_empty + 1, *k_empty = k_full + C::kKv,
            *v_full = k_empty + C::kKv, *v_empty = v_full + C::kKv, *aux_full = v_empty + C::kKv,
-           *aux_empty = aux_full + C::kAux, *s_full = aux_empty + C::kAux, *s_free = s_full + 1, *p_full = s_free + 1,
-           *pv_done = p_full + 1;
+           *aux_empty = aux_full + C::kAux, *s_full = aux_empty + C::kAux, *p_full = s_full + 1, *pv_done = p_full + 1;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(pv_done + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* err = g_attention_err;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kQ; ++i) mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 1);
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
     for (int i = 0; i < C::kKv; ++i) {
       mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], 1), mbar_init(&v_empty[i], 1);
     }
     for (int i = 0; i < C::kAux; ++i) mbar_init(&aux_full[i], 1), mbar_init(&aux_empty[i], 5);
     mbar_init(s_full, 1);
-    mbar_init(s_free, 4);
     mbar_init(p_full, 4);
     mbar_init(pv_done, 1);
     fence_barrier_init();
   }
-  if (warp == 5) tmem_alloc(tslot, 256);
+  if (warp == 5) tmem_alloc(tslot, C::kCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -245,10 +244,10 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   pdl_wait();
   pdl_launch_dependents();
 
-  const int nq = (a.S + 127) / 128, nk = nq;
+  const int nq = (a.S + 127) / 128, nk = (a.S + C::kTK - 1) / C::kTK;
   const int nitems = a.B * a.nh * nq;
   auto info_of = [&](uint32_t g) -> TileInfo* {
-    return reinterpret_cast<TileInfo*>(sAux + (g % C::kAux) * C::kAuxBytes + 4 * C::kWin * 4 + 512);
+    return reinterpret_cast<TileInfo*>(sAux + (g % C::kAux) * C::kAuxBytes + 4 * C::kWin * 4 + C::kTK * 4);
   };
 
   if (warp == 4) {
@@ -262,17 +261,15 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       const int mb = a.mask_seqs == 1 ? 0 : b;
       const float* vec = a.vec ? bias_copy(a, h, 0, 0) : nullptr;
       const float behind = vec ? vec[a.vec_off - a.sat] : 0.0f, ahead = vec ? vec[a.vec_off + a.sat] : 0.0f;
-      const int qs = n % C::kQ;
       if (lane == 0) {
-        ok = mbar_wait(&q_empty[qs], ((n / C::kQ) & 1) ^ 1, err, 201);
+        ok = mbar_wait(q_empty, (n & 1) ^ 1, err, 201);
         if (ok) {
           ++nq_issued;
-          mbar_arrive_expect_tx(&q_full[qs], C::kTile);
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(sQ + qs * C::kTile + c * kRegion, &tq, &q_full[qs], c * 64, i * 128, h, b);
+          mbar_arrive_expect_tx(q_full, C::kQBytes);
+          for (int c = 0; c < D / 64; ++c) tma_load_4d(sQ + c * kRegion, &tq, q_full, c * 64, i * 128, h, b);
         }
       }
-      LiveTiles<2> tiles(a.flags + mb * (a.Sp / kAttnFlagKeys), nk, lane);
+      LiveTiles<C::kTK / kAttnFlagKeys> tiles(a.flags + mb * (a.Sp / kAttnFlagKeys), nk, lane);
       bool mix = false;
       int j = tiles.next(0, mix);
       const bool none = j == nk;
@@ -287,21 +284,21 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
           t.item = n;
           t.bits = (jn == nk ? kLast : 0) | (first ? kFirst : 0);
           t.bias = 0.0f;
-          const int x0 = (j - i) * 128;
+          const int x0 = j * C::kTK - i * 128;   // diagonal of the tile's corner
           bool near = false;
           if (!none) {
             if (mix) t.bits |= kMixed;
             if (vec) {
               if (x0 - 127 >= a.sat) t.bias = ahead;
-              else if (x0 + 127 <= -a.sat) t.bias = behind;
+              else if (x0 + C::kTK - 1 <= -a.sat) t.bias = behind;
               else near = true;
             }
             const int ks = kc % C::kKv;
             if ((ok = mbar_wait(&k_empty[ks], ((kc / C::kKv) & 1) ^ 1, err, 202))) {
               ++nk_issued;
-              mbar_arrive_expect_tx(&k_full[ks], C::kTile);
+              mbar_arrive_expect_tx(&k_full[ks], C::kKvBytes);
               for (int c = 0; c < D / 64; ++c)
-                tma_load_4d(sK + ks * C::kTile + c * kRegion, &tk, &k_full[ks], c * 64, j * 128, h, b);
+                tma_load_4d(sK + ks * C::kKvBytes + c * C::kKvRegion, &tk, &k_full[ks], c * 64, j * C::kTK, h, b);
             }
           }
           if (near) t.bits |= kNear;
@@ -310,19 +307,20 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             *info_of(g) = t;
             const bool mk = !none && mix;
             ++g_issued;
-            mbar_arrive_expect_tx(&aux_full[as], (near ? 4096 : 0) + (mk ? 512 : 0));
+            mbar_arrive_expect_tx(&aux_full[as], (near ? 4 * C::kRun * 4 : 0) + (mk ? C::kTK * 4 : 0));
             if (near)
               for (int s = 0; s < 4; ++s)
-                bulk_load_1d(ax + s * C::kWin * 4, bias_copy(a, h, 0, s) + x0 - 128 + a.vec_off, 1024, &aux_full[as]);
-            if (mk) bulk_load_1d(ax + 4 * C::kWin * 4, a.maskx + (size_t)mb * a.Sp + j * 128, 512, &aux_full[as]);
+                bulk_load_1d(ax + s * C::kWin * 4, bias_copy(a, h, 0, s) + x0 - 128 + a.vec_off, C::kRun * 4,
+                             &aux_full[as]);
+            if (mk) bulk_load_1d(ax + 4 * C::kWin * 4, a.maskx + (size_t)mb * a.Sp + j * C::kTK, C::kTK * 4, &aux_full[as]);
           }
           if (ok && !none) {
             const int ks = kc % C::kKv;
             if ((ok = mbar_wait(&v_empty[ks], ((kc / C::kKv) & 1) ^ 1, err, 204))) {
               ++nv_issued;
-              mbar_arrive_expect_tx(&v_full[ks], C::kTile);
+              mbar_arrive_expect_tx(&v_full[ks], C::kKvBytes);
               for (int c = 0; c < D / 64; ++c)
-                tma_load_4d(sV + ks * C::kTile + c * kRegion, &tv, &v_full[ks], c * 64, j * 128, h, b);
+                tma_load_4d(sV + ks * C::kKvBytes + c * C::kKvRegion, &tv, &v_full[ks], c * 64, j * C::kTK, h, b);
             }
           }
         }
@@ -336,7 +334,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     }
     if (!ok && lane == 0) {
       // a wait gave up: what was issued lands before the block exits
-      drain<C::kQ>(q_full, nq_issued);
+      drain<1>(q_full, nq_issued);
       drain<C::kKv>(k_full, nk_issued);
       drain<C::kKv>(v_full, nv_issued);
       drain<C::kAux>(aux_full, g_issued);
@@ -344,68 +342,51 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   } else if (warp == 5) {
     if (lane == 0) {
       const bool bf = std::is_same<T, bf16_t>::value;
-      const uint32_t id_s = idesc_f16(128, 128, bf, false, false);
+      const uint32_t id_s = idesc_f16(128, C::kTK, bf, false, false);
       const uint32_t id_o = idesc_f16(128, D, bf, false, true);
+      const uint32_t aQ = smem_u32(sQ);
       uint32_t g = 0, kc = 0;
       int n = 0;
       bool ok = true;
-      // P V of the entry before, not yet issued
-      bool pending = false, p_none = false, p_first = false;
-      uint32_t p_kc = 0, p_g = 0;
-      auto pv = [&]() -> bool {
-        pending = false;
-        if (!mbar_wait(p_full, p_g & 1, err, 211)) return false;
-        if (p_none) {
-          mbar_arrive(pv_done);
-          return true;
-        }
-        const int vs = p_kc % C::kKv;
-        if (!mbar_wait(&v_full[vs], (p_kc / C::kKv) & 1, err, 212)) return false;
-        tc_fence_after();
-        const uint32_t aV = smem_u32(sV + vs * C::kTile);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_f16_ts(tmem + C::kO, tmem + C::kP + kk * 8, desc_mn(aV, kk, kRegion), id_o, (!p_first || kk > 0) ? 1u : 0u);
-        mma_commit(pv_done);
-        mma_commit(&v_empty[vs]);
-        return true;
-      };
       for (int it = blockIdx.x; it < nitems && ok; it += gridDim.x, ++n) {
-        const int qs = n % C::kQ;
         bool last = false;
-        while (ok && !last) {
+        for (; ok && !last; ++g) {
           const int as = g % C::kAux;
           if (!(ok = mbar_wait(&aux_full[as], (g / C::kAux) & 1, err, 213))) break;
           const TileInfo t = *info_of(g);
           mbar_arrive(&aux_empty[as]);
           last = t.bits & kLast;
-          const bool none = t.tile < 0;
-          if (D == 128 && pending && !(ok = pv())) break;
-          if ((t.bits & kFirst) && !(ok = mbar_wait(&q_full[qs], (n / C::kQ) & 1, err, 214))) break;
-          if (D == 64 && !(ok = mbar_wait(s_free, (g & 1) ^ 1, err, 215))) break;
-          if (none) {
+          if ((t.bits & kFirst) && !(ok = mbar_wait(q_full, n & 1, err, 214))) break;
+          if (t.tile < 0) {
+            // nothing to multiply: the phases go on
             mbar_arrive(s_full);
-          } else {
-            const int ks = kc % C::kKv;
-            if (!(ok = mbar_wait(&k_full[ks], (kc / C::kKv) & 1, err, 216))) break;
-            tc_fence_after();
-            const uint32_t aQ = smem_u32(sQ + qs * C::kTile), aK = smem_u32(sK + ks * C::kTile);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) mma_f16(tmem, desc_k(aQ, kk, kRegion), desc_k(aK, kk, kRegion), id_s, kk > 0);
-            mma_commit(s_full);
-            mma_commit(&k_empty[ks]);
+            if (!(ok = mbar_wait(p_full, g & 1, err, 211))) break;
+            mbar_arrive(pv_done);
+            continue;
           }
-          if (D == 64 && pending && !(ok = pv())) break;
-          pending = true;
-          p_none = none;
-          p_first = t.bits & kFirst;
-          p_kc = kc;
-          p_g = g;
-          ++g;
-          if (!none) ++kc;
+          const int ks = kc % C::kKv;
+          const uint32_t kp = (kc / C::kKv) & 1;
+          ++kc;
+          if (!(ok = mbar_wait(&k_full[ks], kp, err, 216))) break;
+          tc_fence_after();
+          const uint32_t aK = smem_u32(sK + ks * C::kKvBytes), aV = smem_u32(sV + ks * C::kKvBytes);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_f16(tmem, desc_k(aQ, kk, kRegion), desc_k(aK, kk, C::kKvRegion), id_s, kk > 0);
+          mma_commit(s_full);
+          mma_commit(&k_empty[ks]);
+          // P lies over S, so its product comes before the next Q K^T
+          if (!(ok = mbar_wait(p_full, g & 1, err, 211))) break;
+          if (!(ok = mbar_wait(&v_full[ks], kp, err, 212))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < C::kTK / 16; ++kk)
+            mma_f16_ts(tmem + C::kO, tmem + kk * 8, desc_mn(aV, kk, C::kKvRegion), id_o,
+                       (!(t.bits & kFirst) || kk > 0) ? 1u : 0u);
+          mma_commit(pv_done);
+          mma_commit(&v_empty[ks]);
         }
       }
-      if (ok && pending) pv();
     }
   } else {
     // ---- softmax
@@ -430,7 +411,6 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(&aux_empty[as]);
-            if (D == 64) mbar_arrive(s_free);
             mbar_arrive(p_full);
           }
           continue;
@@ -450,7 +430,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
           mul = 1.0f;
           add = 0.0f;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < C::kTK / 32; ++c) {
             float x[32];
             tmem_ld32_nowait(tmem + lo + c * 32, x);
             tmem_ld_wait();
@@ -483,13 +463,12 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
           tmem_store_wait();
         } else {
 #pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            float x[64];
-            tmem_ld32_nowait(tmem + lo + c * 64, x);
-            tmem_ld32_nowait(tmem + lo + c * 64 + 32, x + 32);
+          for (int c = 0; c < C::kTK / 32; ++c) {
+            float x[32];
+            tmem_ld32_nowait(tmem + lo + c * 32, x);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 64; e += 4) {
+            for (int e = 0; e < 32; e += 4) {
               m0 = max3(m0, x[e], x[e + 1]);
               m1 = max3(m1, x[e + 2], x[e + 3]);
             }
@@ -514,30 +493,21 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         const float sub = add - (ref == -INFINITY ? 0.0f : ref);
         float2 sum0 = f2(0.0f), sum1 = f2(0.0f);
 #pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          float x[64];
-          tmem_ld32_nowait(tmem + lo + c * 64, x);
-          tmem_ld32_nowait(tmem + lo + c * 64 + 32, x + 32);
+        for (int c = 0; c < C::kTK / 32; ++c) {
+          float x[32];
+          tmem_ld32_nowait(tmem + lo + c * 32, x);
           tmem_ld_wait();
-          if (D == 64 && c == 1) {
-            // S has been read: the next Q K^T may start
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(s_free);
-          }
+          uint32_t w[16];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t w[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 y = __ffma2_rn(make_float2(x[half * 32 + 2 * e], x[half * 32 + 2 * e + 1]), f2(mul), f2(sub));
-              const float2 p = make_float2(ex2f(y.x), ex2f(y.y));
-              if (e & 1) sum1 = __fadd2_rn(sum1, p);
-              else sum0 = __fadd2_rn(sum0, p);
-              w[e] = pack2<T>(p.x, p.y);
-            }
-            tmem_st16u(tmem + lo + C::kP + c * 32 + half * 16, w);
+          for (int e = 0; e < 16; ++e) {
+            const float2 y = __ffma2_rn(make_float2(x[2 * e], x[2 * e + 1]), f2(mul), f2(sub));
+            const float2 p = make_float2(ex2f(y.x), ex2f(y.y));
+            if (e & 1) sum1 = __fadd2_rn(sum1, p);
+            else sum0 = __fadd2_rn(sum0, p);
+            w[e] = pack2<T>(p.x, p.y);
           }
+          // over S columns that this thread has read
+          tmem_st16u(tmem + lo + c * 16, w);
         }
         sum0 = __fadd2_rn(sum0, sum1);
         l += sum0.x + sum0.y;
@@ -547,11 +517,10 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         if (lane == 0) mbar_arrive(p_full);
       }
       if (!ok) break;
-      // ---- the item's rows: O / l through the item's Q slot (no product reads it any more)
+      // ---- the item's rows: O / l through the Q tile (no product reads it any more)
       if (!(ok = mbar_wait_warp(pv_done, (g - 1) & 1, err, 225))) break;
       tc_fence_after();
-      const int qs = n % C::kQ;
-      uint8_t* stage = sQ + qs * C::kTile;
+      uint8_t* stage = sQ;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
@@ -582,7 +551,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         for (int c = 0; c < D / 64; ++c) tma_store_4d(&to, stage + c * kRegion, c * 64, i * 128, h, b);
         bulk_commit();
         bulk_wait_read<0>();
-        mbar_arrive(&q_empty[qs]);
+        mbar_arrive(q_empty);
       }
     }
     if (threadIdx.x == 0) bulk_wait_all();
@@ -591,7 +560,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 5) tmem_dealloc(tmem, 256);
+  if (warp == 5) tmem_dealloc(tmem, C::kCols);
 }
 
 // ------------------------------------------------------------------ host side
@@ -635,12 +604,12 @@ template <typename T, int D>
 bool fwd(const AttnOp& a, cudaStream_t s) {
   const bool bf = std::is_same<T, bf16_t>::value;
   CUtensorMap mq, mk, mv, mo;
-  if (!encode(&mq, a.q, a, bf, 128) || !encode(&mk, a.k, a, bf, 128) || !encode(&mv, a.v, a, bf, 128) ||
-      !encode(&mo, a.o, a, bf, 128))
+  if (!encode(&mq, a.q, a, bf, 128) || !encode(&mk, a.k, a, bf, Fwd<D>::kTK) ||
+      !encode(&mv, a.v, a, bf, Fwd<D>::kTK) || !encode(&mo, a.o, a, bf, 128))
     return false;
   cudaFuncSetAttribute(attention_fwd_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Fwd<D>::kSmem);
   const int items = a.B * a.nh * ((a.S + 127) / 128);
-  launch_pdl(attention_fwd_kernel<T, D>, std::min(items, 2 * sm_count()), kFwdThreads, Fwd<D>::kSmem, s, mq, mk, mv, mo, a);
+  launch_pdl(attention_fwd_kernel<T, D>, std::min(items, Fwd<D>::kBlocks * sm_count()), kFwdThreads, Fwd<D>::kSmem, s, mq, mk, mv, mo, a);
   count_launch();
   return true;
 }
