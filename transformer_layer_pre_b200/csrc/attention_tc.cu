@@ -344,48 +344,58 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
       const bool bf = std::is_same<T, bf16_t>::value;
       const uint32_t id_s = idesc_f16(128, C::kTK, bf, false, false);
       const uint32_t id_o = idesc_f16(128, D, bf, false, true);
-      const uint32_t aQ = smem_u32(sQ);
+      // descriptors of slot 0; a K step, a 64-column region and a slot are
+      // offsets of the address field (16-byte units)
+      const uint64_t dq = desc_k(smem_u32(sQ), 0, kRegion), dk = desc_k(smem_u32(sK), 0, C::kKvRegion),
+                     dv = desc_mn(smem_u32(sV), 0, C::kKvRegion);
       uint32_t g = 0, kc = 0;
       int n = 0;
       bool ok = true;
+      TileInfo t;
+      auto next_info = [&](uint32_t e) -> bool {
+        const int as = e % C::kAux;
+        if (!mbar_wait(&aux_full[as], (e / C::kAux) & 1, err, 213)) return false;
+        t = *info_of(e);
+        mbar_arrive(&aux_empty[as]);
+        return t.tile < 0 || mbar_wait(&k_full[kc % C::kKv], (kc / C::kKv) & 1, err, 216);
+      };
       for (int it = blockIdx.x; it < nitems && ok; it += gridDim.x, ++n) {
-        bool last = false;
-        for (; ok && !last; ++g) {
-          const int as = g % C::kAux;
-          if (!(ok = mbar_wait(&aux_full[as], (g / C::kAux) & 1, err, 213))) break;
-          const TileInfo t = *info_of(g);
-          mbar_arrive(&aux_empty[as]);
-          last = t.bits & kLast;
-          if ((t.bits & kFirst) && !(ok = mbar_wait(q_full, n & 1, err, 214))) break;
+        if (!(ok = next_info(g)) || !(ok = mbar_wait(q_full, n & 1, err, 214))) break;
+        for (;; ++g) {
+          const bool last = t.bits & kLast, first = t.bits & kFirst;
           if (t.tile < 0) {
             // nothing to multiply: the phases go on
             mbar_arrive(s_full);
             if (!(ok = mbar_wait(p_full, g & 1, err, 211))) break;
             mbar_arrive(pv_done);
-            continue;
+            break;
           }
           const int ks = kc % C::kKv;
           const uint32_t kp = (kc / C::kKv) & 1;
           ++kc;
-          if (!(ok = mbar_wait(&k_full[ks], kp, err, 216))) break;
           tc_fence_after();
-          const uint32_t aK = smem_u32(sK + ks * C::kKvBytes), aV = smem_u32(sV + ks * C::kKvBytes);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            mma_f16(tmem, desc_k(aQ, kk, kRegion), desc_k(aK, kk, C::kKvRegion), id_s, kk > 0);
+            mma_f16(tmem, dq + (kk >> 2) * (kRegion >> 4) + (kk & 3) * 2,
+                    dk + ks * (C::kKvBytes >> 4) + (kk >> 2) * (C::kKvRegion >> 4) + (kk & 3) * 2, id_s, kk > 0);
           mma_commit(s_full);
           mma_commit(&k_empty[ks]);
+          // what the next tile needs, ahead of the wait for P (an item's first
+          // tile waits for the rows of the item before)
+          if (!last && !(ok = next_info(g + 1))) break;
+          if (!(ok = mbar_wait(&v_full[ks], kp, err, 212))) break;
           // P lies over S, so its product comes before the next Q K^T
           if (!(ok = mbar_wait(p_full, g & 1, err, 211))) break;
-          if (!(ok = mbar_wait(&v_full[ks], kp, err, 212))) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < C::kTK / 16; ++kk)
-            mma_f16_ts(tmem + C::kO, tmem + kk * 8, desc_mn(aV, kk, C::kKvRegion), id_o,
-                       (!(t.bits & kFirst) || kk > 0) ? 1u : 0u);
-          mma_commit(pv_done);
+            mma_f16_ts(tmem + C::kO, tmem + kk * 8, dv + ks * (C::kKvBytes >> 4) + kk * 128, id_o,
+                       (!first || kk > 0) ? 1u : 0u);
+          if (last) mma_commit(pv_done);
           mma_commit(&v_empty[ks]);
+          if (last) break;
         }
+        ++g;
       }
     }
   } else {
@@ -407,7 +417,6 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
         last = t.bits & kLast;
         if (!(ok = mbar_wait_warp(s_full, g & 1, err, 222))) break;
         if (t.tile < 0) {
-          if (g > 0 && !(ok = mbar_wait_warp(pv_done, (g - 1) & 1, err, 223))) break;
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(&aux_empty[as]);
@@ -477,9 +486,7 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
         __syncwarp();
         if (lane == 0) mbar_arrive(&aux_empty[as]);
         const float top = fmaf(fmaxf(m0, m1), mul, add);
-        // P of the tile before has been read, and O holds its product
-        if (g > 0 && !(ok = mbar_wait_warp(pv_done, (g - 1) & 1, err, 224))) break;
-        tc_fence_after();
+        // O holds the products of every tile before: they were issued ahead of this Q K^T
         const float mnew = fmaxf(ref, top);
         if (t.bits & kFirst) {
           ref = mnew;
@@ -518,7 +525,7 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
       }
       if (!ok) break;
       // ---- the item's rows: O / l through the Q tile (no product reads it any more)
-      if (!(ok = mbar_wait_warp(pv_done, (g - 1) & 1, err, 225))) break;
+      if (!(ok = mbar_wait_warp(pv_done, n & 1, err, 225))) break;
       tc_fence_after();
       uint8_t* stage = sQ;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
