@@ -18,13 +18,14 @@ constexpr int kPrepThreads = 256;
 
 // One launch fills the workspace (layout at the top of attention.cuh).
 // Blocks [0, nmask): 256 keys each of maskx and flags.  Then nvec blocks: 256
-// diagonals of one head each, written to every copy.  Then (backward) blocks
+// diagonals of one head each, written to every copy.  Then (backward) nzero
+// blocks that clear dpart, and blocks
 // of 256 / G rows for stats, G lanes per row reading 16 bytes each; rows run
 // (b, token, head) with the head fastest, the order in which O and dO lie in
 // (B, S, heads, d) memory.
 // Bound: HBM in the backward (reads O and dO once), launch latency otherwise.
 template <typename T, int G>
-__global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(const __grid_constant__ AttnOp a, int nmask, int nvec) {
+__global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(const __grid_constant__ AttnOp a, int nmask, int nvec, int nzero) {
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x;
@@ -57,12 +58,10 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(const __grid_co
     const int h = blk / per, X = (blk - h * per) * kPrepThreads + tid;
     if (X >= a.vec_len) return;
     const int x = max(-a.sat, min(a.sat, X - a.vec_off));   // key minus query
-    float v = 0.0f;
-    for (int u = 0; u < a.buckets; ++u)
-      if (x >= a.lo[u] && x - a.lo[u] < a.n[u]) {
-        v = to_f(static_cast<const T*>(a.table)[(size_t)u * a.nh + h]) * kAttnLog2e;
-        break;
-      }
+    int u = 0;
+    while (u < a.buckets - 1 && !(x >= a.lo[u] && x - a.lo[u] < a.n[u])) ++u;
+    const float v = to_f(static_cast<const T*>(a.table)[(size_t)u * a.nh + h]) * kAttnLog2e;
+    if (h == 0) a.bid[X] = (uint8_t)u;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       float* base = a.vec + ((size_t)h * 8 + s) * a.vec_len;
@@ -74,6 +73,12 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(const __grid_co
     return;
   }
   blk -= nvec;
+  if (blk < nzero) {
+    const long long total = (long long)a.B * a.nh * a.ditems * a.buckets;
+    for (long long i = (long long)blk * kPrepThreads + tid; i < total; i += (long long)nzero * kPrepThreads) a.dpart[i] = 0.0f;
+    return;
+  }
+  blk -= nzero;
   constexpr int kEl = 16 / sizeof(T);
   const long long row = (long long)blk * (kPrepThreads / G) + tid / G;
   const long long rows = (long long)a.B * a.Sp * a.nh;
@@ -100,28 +105,34 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(const __grid_co
   if (row < rows && lane == 0) {
     const size_t bh = (size_t)b * a.nh + h;
     float* st = a.stats + bh * 2 * a.Sp;
-    st[i] = i < a.S ? a.lse[bh * a.S + i] * kAttnLog2e : INFINITY;
-    st[a.Sp + i] = i < a.S ? t : 0.0f;
+    st[i] = i < a.S ? -a.lse[bh * a.S + i] * kAttnLog2e : -INFINITY;
+    st[a.Sp + i] = i < a.S ? -t : 0.0f;
   }
 }
 
-// dtable[u, h] (+)= sum over sequences and items of dpart, in a fixed order:
-// one warp per (bucket, head), float64 across the partials.
-__global__ void __launch_bounds__(256) attn_table_grad_kernel(const __grid_constant__ AttnOp a) {
+// dtable[u, h] (+)= sum over sequences and items of dpart, in a fixed order
+// and in float64: a block per head and 32 buckets, a lane per bucket (whole
+// lines of dpart), the rows dealt to the warps.
+constexpr int kTableWarps = 16;
+__global__ void __launch_bounds__(32 * kTableWarps) attn_table_grad_kernel(const __grid_constant__ AttnOp a) {
+  __shared__ double red[kTableWarps][33];
   pdl_wait();
   pdl_launch_dependents();
-  const int w = (blockIdx.x * 256 + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-  if (w >= a.buckets * a.nh) return;
-  const int u = w / a.nh, h = w - u * a.nh;
-  const int rows = a.B * a.ditems;
+  const int h = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, u = blockIdx.y * 32 + lane;
+  const long long rows = (long long)a.B * a.ditems;
   double t = 0.0;
-  for (int r = lane; r < rows; r += 32) {
-    const int b = r / a.ditems, it = r - b * a.ditems;
-    t += (double)a.dpart[(((size_t)b * a.nh + h) * a.ditems + it) * a.buckets + u];
+  if (u < a.buckets) {
+#pragma unroll 4
+    for (long long r = warp; r < rows; r += kTableWarps) {
+      const long long b = r / a.ditems, it = r - b * a.ditems;
+      t += (double)a.dpart[((b * a.nh + h) * a.ditems + it) * a.buckets + u];
+    }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-  if (lane == 0) {
+  red[warp][lane] = t;
+  __syncthreads();
+  if (warp == 0 && u < a.buckets) {
+    t = 0.0;
+    for (int w = 0; w < kTableWarps; ++w) t += red[w][lane];
     float* d = a.dtable + (size_t)u * a.nh + h;
     *d = (float)(a.daccumulate ? (double)*d + t : t);
   }
@@ -131,9 +142,10 @@ template <typename T, int G>
 void prep(const AttnOp& a, bool backward, cudaStream_t s) {
   const int nmask = a.mask_seqs * ((a.Sp + kPrepThreads - 1) / kPrepThreads);
   const int nvec = a.vec ? a.nh * ((a.vec_len + kPrepThreads - 1) / kPrepThreads) : 0;
+  const int nzero = a.dpart ? 64 : 0;
   const long long rows = backward ? (long long)a.B * a.Sp * a.nh : 0;
   const int nrow = (int)((rows + kPrepThreads / G - 1) / (kPrepThreads / G));
-  launch_pdl(attn_prep_kernel<T, G>, nmask + nvec + nrow, kPrepThreads, 0, s, a, nmask, nvec);
+  launch_pdl(attn_prep_kernel<T, G>, nmask + nvec + nzero + nrow, kPrepThreads, 0, s, a, nmask, nvec, nzero);
   count_launch();
 }
 
@@ -246,11 +258,13 @@ tl_status plan(const tl_attention* c, bool backward, char* base, AttnOp& a, size
     a.vec_len = 2 * a.vec_off + 128;
     a.sat = reach;
     a.vec = (float*)(base + take(off, (size_t)a.nh * 8 * a.vec_len * 4));
+    a.bid = (uint8_t*)(base + take(off, a.vec_len));
   }
   if (backward) {
     a.stats = (float*)(base + take(off, (size_t)a.B * a.nh * 2 * a.Sp * 4));
     if (c->bias_table) {
-      a.ditems = (a.S + 63) / 64;   // rows of 64 queries at most
+      // one row per item of 64 queries (float32), or per softmax warp of one of 128
+      a.ditems = c->dtype == TL_F32 ? (a.S + 63) / 64 : a.Sp / 128 * 8;
       a.dpart = (float*)(base + take(off, (size_t)a.B * a.nh * a.ditems * a.buckets * 4));
     }
   }
@@ -269,7 +283,7 @@ void attn_prep_run(int dt, const AttnOp& a, bool backward, cudaStream_t s) {
 }
 
 void attn_table_grad_run(const AttnOp& a, cudaStream_t s) {
-  launch_pdl(attn_table_grad_kernel, (a.buckets * a.nh + 7) / 8, 256, 0, s, a);
+  launch_pdl(attn_table_grad_kernel, dim3(a.nh, (a.buckets + 31) / 32), 32 * kTableWarps, 0, s, a);
   count_launch();
 }
 
@@ -306,7 +320,7 @@ tl_status tl_attention_forward(const tl_attention* c, const tl_heads* q, const t
   ProfScope p_(PC_ATTN_FWD, s);
   attn_prep_run(c->dtype, a, false, s);
   bool ok = true;
-  if (c->dtype == TL_F32) attn_simt_op_fwd_run(c->dtype, a, s);
+  if (c->dtype == TL_F32) attention_f32_fwd_run(a, s);
   else ok = attention_tc_fwd_run(c->dtype, a, s);
   return ok && cudaGetLastError() == cudaSuccess ? TL_OK : TL_ECUDA;
 }
@@ -344,9 +358,11 @@ tl_status tl_attention_backward(const tl_attention* c, const tl_heads* q, const 
   cudaStream_t s = (cudaStream_t)stream;
   ProfScope p_(PC_ATTN_BWD, s);
   attn_prep_run(c->dtype, a, true, s);
-  attn_simt_op_bwd_run(c->dtype, a, s);
+  bool ok = true;
+  if (c->dtype == TL_F32) attention_f32_bwd_run(a, s);
+  else ok = attention_tc_bwd_run(c->dtype, a, s);
   if (dtable) attn_table_grad_run(a, s);
-  return cudaGetLastError() == cudaSuccess ? TL_OK : TL_ECUDA;
+  return ok && cudaGetLastError() == cudaSuccess ? TL_OK : TL_ECUDA;
 }
 
 }  // extern "C"

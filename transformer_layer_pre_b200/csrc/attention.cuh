@@ -10,7 +10,9 @@
 //   maskx  [B or 1][Sp]      log2(e) * mask, -inf for a removed key and past the sequence end
 //   flags  [B or 1][Sp / 64] of each 64 keys: 0 all of maskx is 0, 1 mixed, 2 every key removed
 //   vec    [heads][dirs][4][len] the bias along the diagonals, see bias_at
-//   stats  [B * heads][2][Sp] backward: lse2 (+inf for an empty row and past the end), D = dO.O
+//   bid    [len]             the bucket of each of those diagonals
+//   stats  [B * heads][2][Sp] backward: -lse2 (-inf for an empty row and past the end), -D = -(dO.O)
+//   dpart  backward: partial sums of the bias table's gradient, zeroed
 // with Sp = the sequence length rounded up to 128.
 #pragma once
 
@@ -49,8 +51,9 @@ struct AttnOp {
   float* vec;                // null without a table
   int vec_len, vec_off;      // floats per copy; offset of diagonal 0
   int sat;                   // |j - i| >= sat: the bias no longer depends on the distance
+  uint8_t* bid;
   float* stats;
-  // bias table gradient: partial sums [B * nh][items][buckets], null when not wanted
+  // bias table gradient: partial sums [B * nh][ditems][buckets], null when not wanted
   float* dpart;
   int ditems;                // partial rows per (b, h)
   float* dtable;             // (buckets, nh)
@@ -70,9 +73,11 @@ __device__ __forceinline__ const float* bias_copy(const AttnOp& a, int h, int di
 
 void attn_prep_run(int dt, const AttnOp& a, bool backward, cudaStream_t s);
 void attn_table_grad_run(const AttnOp& a, cudaStream_t s);
-void attn_simt_op_fwd_run(int dt, const AttnOp& a, cudaStream_t s);
-void attn_simt_op_bwd_run(int dt, const AttnOp& a, cudaStream_t s);
+// float32 storage
+void attention_f32_fwd_run(const AttnOp& a, cudaStream_t s);
+void attention_f32_bwd_run(const AttnOp& a, cudaStream_t s);
 // 16-bit storage; false when a tensor could not be described to the TMA unit
 bool attention_tc_fwd_run(int dt, const AttnOp& a, cudaStream_t s);
+bool attention_tc_bwd_run(int dt, const AttnOp& a, cudaStream_t s);
 
 }  // namespace tlp

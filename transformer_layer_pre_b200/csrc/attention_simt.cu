@@ -25,22 +25,20 @@ constexpr int kT = 64;          // rows and columns of a tile
 constexpr int kLd = kT + 4;     // padded row of the transposed operands
 constexpr int kThr = 256;
 
-template <typename T>
-__device__ __forceinline__ const T* row_ptr(const AttnView& v, int b, int h, int i) {
-  return static_cast<const T*>(v.p) + (size_t)b * v.sb + (size_t)h * v.sh + (size_t)i * v.st;
+__device__ __forceinline__ const float* row_ptr(const AttnView& v, int b, int h, int i) {
+  return static_cast<const float*>(v.p) + (size_t)b * v.sb + (size_t)h * v.sh + (size_t)i * v.st;
 }
 
 // Rows r0 .. r0 + 63 of one head, transposed into t[dim][kLd]; zeros past the
 // sequence and past the head dim.
-template <typename T, int D>
+template <int D>
 __device__ __forceinline__ void load_t(float* t, const AttnView& v, int b, int h, int r0, int S, int d) {
   for (int x = threadIdx.x; x < kT * (D / 4); x += kThr) {
     const int r = x % kT, c = (x / kT) * 4;
     float w[4] = {0.f, 0.f, 0.f, 0.f};
     if (r0 + r < S && c < d) {
-      const T* p = row_ptr<T>(v, b, h, r0 + r) + c;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) w[k] = to_f(p[k]);
+      const float4 x = *reinterpret_cast<const float4*>(row_ptr(v, b, h, r0 + r) + c);
+      w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) t[(c + k) * kLd + r] = w[k];
@@ -88,17 +86,17 @@ __device__ __forceinline__ void product(const float* P, const float* B, int ty, 
   }
 }
 
-template <typename T, int D>
+template <int D>
 __device__ __forceinline__ void store_rows(const AttnView& v, int b, int h, int r0, int S, int d, int ty, int tx,
                                            const float (&acc)[4][D / 16], const float (&f)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = r0 + 4 * ty + i;
     if (r >= S) continue;
-    T* p = const_cast<T*>(row_ptr<T>(v, b, h, r));
+    float* p = const_cast<float*>(row_ptr(v, b, h, r));
 #pragma unroll
     for (int m = 0; m < D / 16; ++m)
-      if (tx + 16 * m < d) p[tx + 16 * m] = from_f<T>(acc[i][m] * f[i]);
+      if (tx + 16 * m < d) p[tx + 16 * m] = acc[i][m] * f[i];
   }
 }
 
@@ -108,7 +106,7 @@ __device__ __forceinline__ float bias_at(const AttnOp& a, const float* vec, int 
   return vec[x + a.vec_off];
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThr) attn_fwd_kernel(const __grid_constant__ AttnOp a) {
   extern __shared__ __align__(16) float sm[];
   float* sQ = sm;
@@ -122,7 +120,7 @@ __global__ void __launch_bounds__(kThr) attn_fwd_kernel(const __grid_constant__ 
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int mb = a.mask_seqs == 1 ? 0 : b;
   const float* vec = a.vec ? bias_copy(a, h, 0, 0) : nullptr;
-  load_t<T, D>(sQ, a.q, b, h, q0, a.S, a.d);
+  load_t<D>(sQ, a.q, b, h, q0, a.S, a.d);
   float o[4][D / 16] = {};
   float m[4], l[4];
 #pragma unroll
@@ -130,8 +128,8 @@ __global__ void __launch_bounds__(kThr) attn_fwd_kernel(const __grid_constant__ 
   for (int k0 = 0; k0 < a.S; k0 += kT) {
     if (a.flags[mb * (a.Sp / kAttnFlagKeys) + k0 / kAttnFlagKeys] == 2) continue;
     __syncthreads();
-    load_t<T, D>(sK, a.k, b, h, k0, a.S, a.d);
-    load_t<T, D>(sV, a.v, b, h, k0, a.S, a.d);
+    load_t<D>(sK, a.k, b, h, k0, a.S, a.d);
+    load_t<D>(sV, a.v, b, h, k0, a.S, a.d);
     __syncthreads();
     float s[4][4];
     scores<D>(sQ, sK, ty, tx, s);
@@ -177,10 +175,10 @@ __global__ void __launch_bounds__(kThr) attn_fwd_kernel(const __grid_constant__ 
     const int r = q0 + 4 * ty + i;
     if (tx == 0 && r < a.S) a.lse[(size_t)bh * a.S + r] = l[i] == 0.0f ? INFINITY : (m[i] + log2f(l[i])) * kAttnLn2;
   }
-  store_rows<T, D>(a.o, b, h, q0, a.S, a.d, ty, tx, o, f);
+  store_rows<D>(a.o, b, h, q0, a.S, a.d, ty, tx, o, f);
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThr) attn_bwd_kernel(const __grid_constant__ AttnOp a) {
   extern __shared__ __align__(16) float sm[];
   float* sA1 = sm;                 // stationary rows: K, V or Q, dO
@@ -201,20 +199,20 @@ __global__ void __launch_bounds__(kThr) attn_bwd_kernel(const __grid_constant__ 
   const float* vec = a.vec ? bias_copy(a, h, 0, 0) : nullptr;
   const float* mask = a.maskx + (size_t)mb * a.Sp;
   const int* flags = a.flags + mb * (a.Sp / kAttnFlagKeys);
-  const float* lse2 = a.stats + (size_t)bh * 2 * a.Sp;
-  const float* dv = lse2 + a.Sp;
+  const float* nlse = a.stats + (size_t)bh * 2 * a.Sp;
+  const float* nd = nlse + a.Sp;
   float acc1[4][D / 16] = {}, acc2[4][D / 16] = {};
   const bool grad = !keys && a.dpart;
   if (grad)
     for (int u = threadIdx.x; u < a.buckets; u += kThr) sBins[u] = 0.0f;
-  load_t<T, D>(sA1, keys ? a.k : a.q, b, h, r0, a.S, a.d);
-  load_t<T, D>(sA2, keys ? a.v : a.dout, b, h, r0, a.S, a.d);
+  load_t<D>(sA1, keys ? a.k : a.q, b, h, r0, a.S, a.d);
+  load_t<D>(sA2, keys ? a.v : a.dout, b, h, r0, a.S, a.d);
   const bool none = keys && flags[r0 / kAttnFlagKeys] == 2;   // dK = dV = 0
   for (int c0 = 0; c0 < a.S && !none; c0 += kT) {
     if (!keys && flags[c0 / kAttnFlagKeys] == 2) continue;
     __syncthreads();
-    load_t<T, D>(sB1, keys ? a.q : a.k, b, h, c0, a.S, a.d);
-    load_t<T, D>(sB2, keys ? a.dout : a.v, b, h, c0, a.S, a.d);
+    load_t<D>(sB1, keys ? a.q : a.k, b, h, c0, a.S, a.d);
+    load_t<D>(sB2, keys ? a.dout : a.v, b, h, c0, a.S, a.d);
     __syncthreads();
     float s[4][4], dp[4][4];
     scores<D>(sA1, sB1, ty, tx, s);
@@ -226,11 +224,11 @@ __global__ void __launch_bounds__(kThr) attn_bwd_kernel(const __grid_constant__ 
         const int row = r0 + 4 * ty + i, col = c0 + 4 * tx + j;
         const int qi = keys ? col : row, kj = keys ? row : col;   // both below Sp
         const float bias = vec ? bias_at(a, vec, kj - qi) : 0.0f;
-        const float mk = mask[kj], ls = lse2[qi];
-        // an empty row has lse2 = +inf: p = 0
-        const float p = mk == -INFINITY || ls == INFINITY ? 0.0f : exp2f(fmaf(s[i][j], a.c2, bias + mk) - ls);
+        const float mk = mask[kj], nl = nlse[qi];
+        // a removed key, an empty row: p = 0
+        const float p = mk == -INFINITY || nl == -INFINITY ? 0.0f : exp2f(fmaf(s[i][j], a.c2, bias + mk) + nl);
         s[i][j] = p;
-        dp[i][j] = p == 0.0f ? 0.0f : p * (dp[i][j] - dv[qi]);
+        dp[i][j] = p == 0.0f ? 0.0f : p * (dp[i][j] + nd[qi]);
       }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -262,8 +260,8 @@ __global__ void __launch_bounds__(kThr) attn_bwd_kernel(const __grid_constant__ 
     }
   }
   const float one[4] = {1.f, 1.f, 1.f, 1.f}, sc[4] = {a.scale, a.scale, a.scale, a.scale};
-  store_rows<T, D>(keys ? a.dk : a.dq, b, h, r0, a.S, a.d, ty, tx, acc1, sc);
-  if (keys) store_rows<T, D>(a.dv, b, h, r0, a.S, a.d, ty, tx, acc2, one);
+  store_rows<D>(keys ? a.dk : a.dq, b, h, r0, a.S, a.d, ty, tx, acc1, sc);
+  if (keys) store_rows<D>(a.dv, b, h, r0, a.S, a.d, ty, tx, acc2, one);
   if (grad) {
     __syncthreads();
     for (int u = threadIdx.x; u < a.buckets; u += kThr)
@@ -271,48 +269,35 @@ __global__ void __launch_bounds__(kThr) attn_bwd_kernel(const __grid_constant__ 
   }
 }
 
-template <typename T, int D>
+template <int D>
 void fwd(const AttnOp& a, cudaStream_t s) {
   constexpr int smem = (3 * D + kT) * kLd * 4;
-  cudaFuncSetAttribute(attn_fwd_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  launch_pdl(attn_fwd_kernel<T, D>, a.B * a.nh * ((a.S + kT - 1) / kT), kThr, smem, s, a);
+  cudaFuncSetAttribute(attn_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  launch_pdl(attn_fwd_kernel<D>, a.B * a.nh * ((a.S + kT - 1) / kT), kThr, smem, s, a);
   count_launch();
 }
-template <typename T, int D>
+template <int D>
 void bwd(const AttnOp& a, cudaStream_t s) {
   constexpr int smem = (4 * D + 2 * kT) * kLd * 4 + kAttnMaxBuckets * 4;
-  cudaFuncSetAttribute(attn_bwd_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  launch_pdl(attn_bwd_kernel<T, D>, 2 * a.B * a.nh * ((a.S + kT - 1) / kT), kThr, smem, s, a);
+  cudaFuncSetAttribute(attn_bwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  launch_pdl(attn_bwd_kernel<D>, 2 * a.B * a.nh * ((a.S + kT - 1) / kT), kThr, smem, s, a);
   count_launch();
-}
-
-template <typename T>
-void fwd_t(const AttnOp& a, cudaStream_t s) {
-  if (a.d <= 16) fwd<T, 16>(a, s);
-  else if (a.d <= 32) fwd<T, 32>(a, s);
-  else if (a.d <= 64) fwd<T, 64>(a, s);
-  else fwd<T, 128>(a, s);
-}
-template <typename T>
-void bwd_t(const AttnOp& a, cudaStream_t s) {
-  if (a.d <= 16) bwd<T, 16>(a, s);
-  else if (a.d <= 32) bwd<T, 32>(a, s);
-  else if (a.d <= 64) bwd<T, 64>(a, s);
-  else bwd<T, 128>(a, s);
 }
 
 }  // namespace
 
-void attn_simt_op_fwd_run(int dt, const AttnOp& a, cudaStream_t s) {
-  if (dt == DT_F32) fwd_t<float>(a, s);
-  else if (dt == DT_F16) fwd_t<half_t>(a, s);
-  else fwd_t<bf16_t>(a, s);
+void attention_f32_fwd_run(const AttnOp& a, cudaStream_t s) {
+  if (a.d <= 16) fwd<16>(a, s);
+  else if (a.d <= 32) fwd<32>(a, s);
+  else if (a.d <= 64) fwd<64>(a, s);
+  else fwd<128>(a, s);
 }
 
-void attn_simt_op_bwd_run(int dt, const AttnOp& a, cudaStream_t s) {
-  if (dt == DT_F32) bwd_t<float>(a, s);
-  else if (dt == DT_F16) bwd_t<half_t>(a, s);
-  else bwd_t<bf16_t>(a, s);
+void attention_f32_bwd_run(const AttnOp& a, cudaStream_t s) {
+  if (a.d <= 16) bwd<16>(a, s);
+  else if (a.d <= 32) bwd<32>(a, s);
+  else if (a.d <= 64) bwd<64>(a, s);
+  else bwd<128>(a, s);
 }
 
 }  // namespace tlp

@@ -570,6 +570,529 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
   if (warp == 5) tmem_dealloc(tmem, C::kCols);
 }
 
+// ============================================================================ backward
+// One block per SM walks items of 128 stationary rows against moving tiles of
+// 64 columns.  Key items (all of them first): rows K and V, columns Q and dO,
+//   S^T = K Q^T, dP^T = V dO^T;  dV += P^T dO, dK += dS^T Q
+// query items: rows Q and dO, columns K and V,
+//   S = Q K^T, dP = dO V^T;  dQ += dS K, and dS summed into the bias gradient.
+// S and dP are formed twice (7 products instead of 5), and in return no sum
+// is shared between blocks: no atomics, every gradient bitwise reproducible.
+//
+// Warps 0-3 and 4-7 take the moving tiles in turn (one row, that is one TMEM
+// lane, per thread), so one tile's exponentials run while the other's
+// products do; 8-11 write the finished rows out; 12: TMA; 13: MMA.  P and dS
+// (rounded to the storage type, at most half a step) overwrite S and dP in
+// TMEM and are the A operands of the second pair of products from there, so
+// they never touch shared memory.
+// TMEM: per softmax group S, dP (64 columns each); from 256 on the sums, two
+// sets of them for D = 64, so the next item starts while one is written out.
+template <int D>
+struct Bwd {
+  static constexpr int kSt = D / 64 * kRegion;                      // a stationary tile
+  static constexpr int kMvRegion = 64 * 128;
+  static constexpr int kMv = D / 64 * kMvRegion;                    // a moving tile
+  static constexpr int kNs = D == 64 ? 4 : 2;                       // moving stages
+  static constexpr int kNa = 4;                                     // tile descriptions
+  static constexpr int kAcc = D == 64 ? 2 : 1;                      // sets of sums
+  static constexpr int kRun = 192, kWin = 200;
+  static constexpr int kVecA = 4 * kWin * 4, kVecB = kVecA + 256, kInfo = kVecB + 256;
+  static constexpr int kAuxBytes = kInfo + 16;
+  static constexpr int kStAux = 2 * 128 * 4 + 16;                   // row vectors, empty flag
+  static constexpr int kChain = 48;                                 // floats of a diagonal chain, see bias_diagonals
+  static constexpr int kSmem = 4 * kSt + 2 * kNs * kMv + kNa * kAuxBytes + 2 * kStAux + 8 * kAttnMaxBuckets * 4 +
+                               8 * 4 * kChain * 4 + 320;
+};
+static_assert(Bwd<128>::kSmem <= 227 * 1024, "the backward's shared memory exceeds a block's maximum");
+constexpr int kBwdThreads = 448;
+
+// Sums the diagonals of a warp's 32 rows x 16 columns (v: this lane's row).
+// Diagonal t - lane moves up one lane per column, so the running sums are
+// shifted along; the one that leaves at lane 31 is done and goes to
+// out[t], the 32 left at the end to out[16 ..], in order of the diagonal:
+// out[y] is diagonal y - 31.
+__device__ __forceinline__ void diagonal_chain(const float* v, float* out, int lane) {
+  float s = 0.0f;
+#pragma unroll
+  for (int t = 0; t < 16; ++t) {
+    s += v[t];
+    if (t < 15) {
+      if (lane == 31) out[t] = s;
+      s = __shfl_up_sync(0xffffffffu, s, 1);
+      if (lane == 0) s = 0.0f;
+    }
+  }
+  out[46 - lane] = s;
+}
+
+// One warp's 32 rows x 64 columns of dS, from its four chains into its bins:
+// each of the 95 diagonals is the sum of the chains that cross it; those of one
+// bucket are neighbours and are summed by a segmented scan.  bid: the bucket of
+// diagonal 0 of the block of rows (column 0, row 0 of the warp).
+__device__ __forceinline__ void bin_diagonals(const float* chains, int chain_stride, const uint8_t* bid, float* bins,
+                                              int lane) {
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    const int y = lane + 32 * k;            // diagonal y - 31
+    float s = 0.0f;
+    int u = 256;
+    if (y < 95) {
+      u = bid[y - 31];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int z = y - 16 * c;
+        if (z >= 0 && z < 47) s += chains[c * chain_stride + z];
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float s2 = __shfl_up_sync(0xffffffffu, s, o);
+      const int u2 = __shfl_up_sync(0xffffffffu, u, o);
+      if (lane >= o && u2 == u) s += s2;
+    }
+    const int next = __shfl_down_sync(0xffffffffu, u, 1);
+    if (u < 256 && (lane == 31 || next != u)) bins[u] += s;
+    __syncwarp();
+  }
+}
+
+// A tile's scores and dP, 64 columns of this thread's row, into P and dS.
+// ax: the tile's staged vectors; row: what this row adds (log2 units, bias of
+// a far tile included), nd_row: -D of a query row.
+template <typename T, bool KEYS, bool NEAR, bool MIX>
+__device__ __forceinline__ void bwd_tile(uint32_t tS, const uint8_t* ax, int win, const float* vecA, const float* vecB,
+                                         float c2, float row, float nd_row, int r, bool grad, float& far_sum,
+                                         float* chains, int lane) {
+  const int start = 128 - r;
+  const float* wnd = reinterpret_cast<const float*>(ax) + (start & 3) * win + (start & ~3);
+  float2 fs = f2(0.0f);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    float s[32], dp[32];
+    tmem_ld32_nowait(tS + c * 32, s);
+    tmem_ld32_nowait(tS + 64 + c * 32, dp);
+    tmem_ld_wait();
+    uint32_t wp[16], wd[16];
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+      float2 add0 = f2(row), add1 = f2(row), nd0 = f2(nd_row), nd1 = f2(nd_row);
+      if (KEYS || MIX) {
+        const float4 w = *reinterpret_cast<const float4*>(vecA + c * 32 + e);
+        add0 = __fadd2_rn(add0, make_float2(w.x, w.y));
+        add1 = __fadd2_rn(add1, make_float2(w.z, w.w));
+      }
+      if (KEYS) {
+        const float4 w = *reinterpret_cast<const float4*>(vecB + c * 32 + e);
+        nd0 = make_float2(w.x, w.y);
+        nd1 = make_float2(w.z, w.w);
+      }
+      if (NEAR) {
+        const float4 w = *reinterpret_cast<const float4*>(wnd + c * 32 + e);
+        add0 = __fadd2_rn(add0, make_float2(w.x, w.y));
+        add1 = __fadd2_rn(add1, make_float2(w.z, w.w));
+      }
+      const float2 x0 = __ffma2_rn(make_float2(s[e], s[e + 1]), f2(c2), add0);
+      const float2 x1 = __ffma2_rn(make_float2(s[e + 2], s[e + 3]), f2(c2), add1);
+      const float2 p0 = make_float2(ex2f(x0.x), ex2f(x0.y)), p1 = make_float2(ex2f(x1.x), ex2f(x1.y));
+      const float2 d0 = __fmul2_rn(p0, __fadd2_rn(make_float2(dp[e], dp[e + 1]), nd0));
+      const float2 d1 = __fmul2_rn(p1, __fadd2_rn(make_float2(dp[e + 2], dp[e + 3]), nd1));
+      if (KEYS) {
+        wp[e / 2] = pack2<T>(p0.x, p0.y);
+        wp[e / 2 + 1] = pack2<T>(p1.x, p1.y);
+      }
+      wd[e / 2] = pack2<T>(d0.x, d0.y);
+      wd[e / 2 + 1] = pack2<T>(d1.x, d1.y);
+      if (!KEYS) {
+        if (NEAR) {
+          dp[e] = d0.x, dp[e + 1] = d0.y, dp[e + 2] = d1.x, dp[e + 3] = d1.y;
+        } else {
+          fs = __fadd2_rn(fs, __fadd2_rn(d0, d1));
+        }
+      }
+    }
+    // over S and dP columns that this thread has read
+    if (KEYS) tmem_st16u(tS + c * 16, wp);
+    tmem_st16u(tS + 64 + c * 16, wd);
+    if (!KEYS && NEAR && grad) {
+      diagonal_chain(dp, chains + (2 * c) * Bwd<64>::kChain, lane);
+      diagonal_chain(dp + 16, chains + (2 * c + 1) * Bwd<64>::kChain, lane);
+    }
+  }
+  far_sum += fs.x + fs.y;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    attention_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                         const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
+                         const __grid_constant__ CUtensorMap tdq, const __grid_constant__ CUtensorMap tdk,
+                         const __grid_constant__ CUtensorMap tdv, const __grid_constant__ AttnOp a) {
+  using C = Bwd<D>;
+  // the only shared memory of the kernel: its start is 1024-byte aligned
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sSt = smem_raw;                                  // [2] x (A1, A2)
+  uint8_t* sMv = sSt + 4 * C::kSt;                          // [kNs] x (B1, B2)
+  uint8_t* sAux = sMv + 2 * C::kNs * C::kMv;                // [kNa]
+  uint8_t* sStAux = sAux + C::kNa * C::kAuxBytes;           // [2]
+  float* sBins = reinterpret_cast<float*>(sStAux + 2 * C::kStAux);
+  float* sChains = sBins + 8 * kAttnMaxBuckets;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sChains + 8 * 4 * C::kChain);
+  uint64_t *st_full = bar, *st_empty = st_full + 2, *mv_full = st_empty + 2, *mv_empty = mv_full + C::kNs,
+           *aux_full = mv_empty + C::kNs, *aux_empty = aux_full + C::kNa, *s_full = aux_empty + C::kNa,
+           *p_full = s_full + 2, *acc_full = p_full + 2, *acc_free = acc_full + C::kAcc;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(acc_free + C::kAcc);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int* err = g_attention_err;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&st_full[i], 1), mbar_init(&st_empty[i], 1);
+      mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 4);
+    }
+    for (int i = 0; i < C::kNs; ++i) mbar_init(&mv_full[i], 1), mbar_init(&mv_empty[i], 1);
+    for (int i = 0; i < C::kNa; ++i) mbar_init(&aux_full[i], 1), mbar_init(&aux_empty[i], 5);
+    for (int i = 0; i < C::kAcc; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_free[i], 4);
+    fence_barrier_init();
+  }
+  if (warp == 13) tmem_alloc(tslot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  const int nr = (a.S + 127) / 128, nm = (a.S + 63) / 64;
+  const int items = a.B * a.nh * nr;
+  auto info_of = [&](uint32_t g) -> TileInfo* {
+    return reinterpret_cast<TileInfo*>(sAux + (g % C::kNa) * C::kAuxBytes + C::kInfo);
+  };
+  auto row_vec = [&](int n) { return reinterpret_cast<float*>(sStAux + (n & 1) * C::kStAux); };
+  auto none_flag = [&](int n) { return reinterpret_cast<int*>(sStAux + (n & 1) * C::kStAux + 1024); };
+
+  if (warp == 12) {
+    // ---- producer
+    uint32_t g = 0, mc = 0;
+    uint32_t st_issued = 0, mv_issued = 0, aux_issued = 0;
+    int n = 0;
+    bool ok = true;
+    for (int it = blockIdx.x; it < 2 * items && ok; it += gridDim.x, ++n) {
+      const bool keys = it < items;
+      const int x = keys ? it : it - items, bh = x / nr, ri = x - bh * nr, b = bh / a.nh, h = bh - b * a.nh;
+      const int mb = a.mask_seqs == 1 ? 0 : b;
+      const int* flags = a.flags + mb * (a.Sp / kAttnFlagKeys);
+      const float* vec = a.vec ? bias_copy(a, h, 0, 0) : nullptr;
+      const float behind = vec ? vec[a.vec_off - a.sat] : 0.0f, ahead = vec ? vec[a.vec_off + a.sat] : 0.0f;
+      LiveTiles<1> tiles(flags, nm, lane);
+      bool mix = false;
+      int j = keys ? (flags[2 * ri] == 2 && flags[2 * ri + 1] == 2 ? nm : 0) : tiles.next(0, mix);
+      const bool none = j == nm;
+      const int slot = n & 1;
+      if (lane == 0 && (ok = mbar_wait(&st_empty[slot], ((n >> 1) & 1) ^ 1, err, 301))) {
+        *none_flag(n) = none;
+        ++st_issued;
+        mbar_arrive_expect_tx(&st_full[slot], 2 * C::kSt + (keys ? 512 : 1024));
+        uint8_t* st = sSt + slot * 2 * C::kSt;
+        for (int c = 0; c < D / 64; ++c)
+          for (int t = 0; t < 2; ++t) {
+            tma_load_4d(st + c * kRegion + t * 8192, keys ? &tk : &tq, &st_full[slot], c * 64, ri * 128 + t * 64, h, b);
+            tma_load_4d(st + C::kSt + c * kRegion + t * 8192, keys ? &tv : &tdo, &st_full[slot], c * 64,
+                        ri * 128 + t * 64, h, b);
+          }
+        if (keys) {
+          bulk_load_1d(row_vec(n), a.maskx + (size_t)mb * a.Sp + ri * 128, 512, &st_full[slot]);
+        } else {
+          bulk_load_1d(row_vec(n), a.stats + (size_t)bh * 2 * a.Sp + ri * 128, 512, &st_full[slot]);
+          bulk_load_1d(row_vec(n) + 128, a.stats + (size_t)bh * 2 * a.Sp + a.Sp + ri * 128, 512, &st_full[slot]);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      bool first = true;
+      do {
+        bool nmix = false;
+        const int jn = none ? nm : (keys ? j + 1 : tiles.next(j + 1, nmix));
+        if (lane == 0 && ok) {
+          const int as = g % C::kNa;
+          TileInfo t;
+          t.tile = none ? -1 : j;
+          t.item = n;
+          t.bits = (jn == nm ? kLast : 0) | (first ? kFirst : 0) | (keys ? kKeys : 0);
+          t.bias = 0.0f;
+          // diagonal of the tile's corner, column minus row
+          const int x0 = j * 64 - ri * 128;
+          if (!none) {
+            if (vec) {
+              // key minus query: the columns are the keys, or the rows are
+              const int lo = keys ? -(x0 + 63) : x0 - 127, hi = keys ? 127 - x0 : x0 + 63;
+              if (lo >= a.sat) t.bias = ahead, t.bits |= kAhead;
+              else if (hi <= -a.sat) t.bias = behind;
+              else t.bits |= kNear;
+            }
+            if (mix && !keys) t.bits |= kMixed;
+          }
+          if ((ok = mbar_wait(&aux_empty[as], ((g / C::kNa) & 1) ^ 1, err, 302))) {
+            uint8_t* ax = sAux + as * C::kAuxBytes;
+            *info_of(g) = t;
+            const bool near = t.bits & kNear, va = !none && (keys || near || (t.bits & kMixed));
+            ++aux_issued;
+            mbar_arrive_expect_tx(&aux_full[as], (near ? 4 * C::kRun * 4 : 0) + (va ? 256 : 0) + (keys && !none ? 256 : 0));
+            if (near)
+              for (int s = 0; s < 4; ++s)
+                bulk_load_1d(ax + s * C::kWin * 4, bias_copy(a, h, keys ? 1 : 0, s) + x0 - 128 + a.vec_off, C::kRun * 4,
+                             &aux_full[as]);
+            if (va)
+              bulk_load_1d(ax + C::kVecA,
+                           (keys ? a.stats + (size_t)bh * 2 * a.Sp : a.maskx + (size_t)mb * a.Sp) + j * 64, 256,
+                           &aux_full[as]);
+            if (keys && !none)
+              bulk_load_1d(ax + C::kVecB, a.stats + (size_t)bh * 2 * a.Sp + a.Sp + j * 64, 256, &aux_full[as]);
+          }
+          if (ok && !none) {
+            const int ms = mc % C::kNs;
+            if ((ok = mbar_wait(&mv_empty[ms], ((mc / C::kNs) & 1) ^ 1, err, 303))) {
+              ++mv_issued;
+              mbar_arrive_expect_tx(&mv_full[ms], 2 * C::kMv);
+              uint8_t* mv = sMv + ms * 2 * C::kMv;
+              for (int c = 0; c < D / 64; ++c) {
+                tma_load_4d(mv + c * C::kMvRegion, keys ? &tq : &tk, &mv_full[ms], c * 64, j * 64, h, b);
+                tma_load_4d(mv + C::kMv + c * C::kMvRegion, keys ? &tdo : &tv, &mv_full[ms], c * 64, j * 64, h, b);
+              }
+            }
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        first = false;
+        ++g;
+        if (!none) ++mc;
+        j = jn;
+        mix = nmix;
+      } while (ok && j < nm);
+    }
+    // the end, for either softmax group (the MMA thread stops at the first)
+    for (int e = 0; e < 2 && ok && lane == 0; ++e, ++g) {
+      if (!(ok = mbar_wait(&aux_empty[g % C::kNa], ((g / C::kNa) & 1) ^ 1, err, 304))) break;
+      TileInfo t = {-1, kEnd, 0.0f, -1};
+      *info_of(g) = t;
+      ++aux_issued;
+      mbar_arrive(&aux_full[g % C::kNa]);
+    }
+    if (!ok && lane == 0) {
+      drain<2>(st_full, st_issued);
+      drain<C::kNs>(mv_full, mv_issued);
+      drain<C::kNa>(aux_full, aux_issued);
+    }
+  } else if (warp == 13) {
+    if (lane == 0) {
+      const bool bf = std::is_same<T, bf16_t>::value;
+      const uint32_t id_s = idesc_f16(128, 64, bf, false, false);
+      const uint32_t id_a = idesc_f16(128, D, bf, false, true);
+      const uint64_t dst = desc_k(smem_u32(sSt), 0, kRegion), dmv = desc_k(smem_u32(sMv), 0, C::kMvRegion),
+                     dmn = desc_mn(smem_u32(sMv), 0, C::kMvRegion);
+      uint32_t g = 0, mc = 0;
+      bool ok = true, pending = false;
+      TileInfo p = {-1, 0, 0.0f, 0};   // the tile whose second products are not issued yet
+      uint32_t p_g = 0, p_mc = 0;
+      auto sums = [&]() -> bool {
+        const int w = p_g & 1, ab = p.item % C::kAcc;
+        if (!mbar_wait(&p_full[w], (p_g >> 1) & 1, err, 311)) return false;
+        if ((p.bits & kFirst) && !mbar_wait(&acc_free[ab], ((p.item / C::kAcc) & 1) ^ 1, err, 312)) return false;
+        if (p.tile < 0) {
+          mbar_arrive(&acc_full[ab]);
+          return true;
+        }
+        tc_fence_after();
+        const int ms = p_mc % C::kNs;
+        const uint32_t acc1 = tmem + 256 + ab * 2 * D, acc2 = acc1 + D, tS = tmem + w * 128;
+        const uint64_t b1 = dmn + ms * (2 * C::kMv >> 4), b2 = b1 + (C::kMv >> 4);
+        const uint32_t more = p.bits & kFirst ? 0u : 1u;
+        if (p.bits & kKeys) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) mma_f16_ts(acc2, tS + kk * 8, b2 + kk * 128, id_a, more | (kk > 0));
+        }
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) mma_f16_ts(acc1, tS + 64 + kk * 8, b1 + kk * 128, id_a, more | (kk > 0));
+        mma_commit(&mv_empty[ms]);
+        if (p.bits & kLast) mma_commit(&acc_full[ab]);
+        return true;
+      };
+      for (;; ++g) {
+        const int as = g % C::kNa, w = g & 1;
+        if (!(ok = mbar_wait(&aux_full[as], (g / C::kNa) & 1, err, 313))) break;
+        const TileInfo t = *info_of(g);
+        mbar_arrive(&aux_empty[as]);
+        if (t.bits & kEnd) break;
+        const int slot = t.item & 1;
+        if ((t.bits & kFirst) && !(ok = mbar_wait(&st_full[slot], (t.item >> 1) & 1, err, 314))) break;
+        if (t.tile < 0) {
+          mbar_arrive(&s_full[w]);
+        } else {
+          const int ms = mc % C::kNs;
+          if (!(ok = mbar_wait(&mv_full[ms], (mc / C::kNs) & 1, err, 315))) break;
+          tc_fence_after();
+          const uint64_t a1 = dst + slot * (2 * C::kSt >> 4), a2 = a1 + (C::kSt >> 4);
+          const uint64_t b1 = dmv + ms * (2 * C::kMv >> 4), b2 = b1 + (C::kMv >> 4);
+          const uint32_t tS = tmem + w * 128;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_f16(tS, a1 + (kk >> 2) * (kRegion >> 4) + (kk & 3) * 2, b1 + (kk >> 2) * (C::kMvRegion >> 4) + (kk & 3) * 2,
+                    id_s, kk > 0);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_f16(tS + 64, a2 + (kk >> 2) * (kRegion >> 4) + (kk & 3) * 2,
+                    b2 + (kk >> 2) * (C::kMvRegion >> 4) + (kk & 3) * 2, id_s, kk > 0);
+          mma_commit(&s_full[w]);
+        }
+        if (pending && !(ok = sums())) break;
+        pending = true;
+        p = t;
+        p_g = g;
+        p_mc = mc;
+        if (t.tile >= 0) ++mc;
+      }
+      if (ok && pending) sums();
+    }
+  } else if (warp >= 8) {
+    // ---- finished rows: TMEM -> scale -> the item's own stationary tiles (no
+    // product reads them any more) -> TMA store
+    const int r = threadIdx.x - 256;
+    const uint32_t lo = (uint32_t)((warp & 3) * 32) << 16;
+    bool ok = true;
+    int n = 0;
+    for (int it = blockIdx.x; it < 2 * items && ok; it += gridDim.x, ++n) {
+      const bool keys = it < items;
+      const int x = keys ? it : it - items, bh = x / nr, ri = x - bh * nr, b = bh / a.nh, h = bh - b * a.nh;
+      const int slot = n & 1, ab = n % C::kAcc;
+      if (!(ok = mbar_wait_warp(&st_full[slot], (n >> 1) & 1, err, 321))) break;
+      const bool none = *none_flag(n) != 0;
+      if (!(ok = mbar_wait_warp(&acc_full[ab], (n / C::kAcc) & 1, err, 322))) break;
+      tc_fence_after();
+      uint8_t* st = sSt + slot * 2 * C::kSt;
+#pragma unroll 1
+      for (int q = 0; q < (keys ? 2 : 1); ++q) {
+        const float f = q == 0 ? a.scale : 1.0f;
+        uint8_t* out = st + q * C::kSt;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          float v[32];
+          tmem_ld32_nowait(tmem + lo + 256 + ab * 2 * D + q * D + c * 32, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = none ? 0u : pack2<T>(v[e * 8 + 2 * k] * f, v[e * 8 + 2 * k + 1] * f);
+            const int ch = c * 4 + e;
+            *reinterpret_cast<uint4*>(out + (ch >> 3) * kRegion + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_free[ab]);
+      fence_proxy_async_smem();
+      named_barrier(1, 128);
+      if (r == 0) {
+        for (int c = 0; c < D / 64; ++c) {
+          tma_store_4d(keys ? &tdk : &tdq, st + c * kRegion, c * 64, ri * 128, h, b);
+          if (keys) tma_store_4d(&tdv, st + C::kSt + c * kRegion, c * 64, ri * 128, h, b);
+        }
+        bulk_commit();
+        bulk_wait_read<0>();
+        mbar_arrive(&st_empty[slot]);
+      }
+    }
+    if (r == 0) bulk_wait_all();
+    __syncwarp();
+  } else {
+    // ---- softmax groups
+    const int wg = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t tS = tmem + wg * 128 + ((uint32_t)((warp & 3) * 32) << 16);
+    const float c2 = a.c2;
+    float* bins = sBins + warp * kAttnMaxBuckets;
+    float* chains = sChains + warp * 4 * C::kChain;
+    const bool want = a.dpart != nullptr;
+    if (want)
+      for (int u = lane; u < a.buckets; u += 32) bins[u] = 0.0f;
+    __syncwarp();
+    int cur = -1, row0 = 0;
+    size_t part = 0;               // this warp's row of dpart for the current item
+    bool grad = false;
+    float add = 0.0f, nd = 0.0f, far_behind = 0.0f, far_ahead = 0.0f;
+    // the item's bias gradient: this warp's share
+    auto flush = [&]() {
+      const float fb = warp_sum(far_behind), fa = warp_sum(far_ahead);
+      if (lane == 0) {
+        bins[a.buckets / 2 - 1] += fb;
+        bins[a.buckets - 1] += fa;
+      }
+      __syncwarp();
+      for (int u = lane; u < a.buckets; u += 32) {
+        a.dpart[part + u] = bins[u];
+        bins[u] = 0.0f;
+      }
+      __syncwarp();
+      far_behind = far_ahead = 0.0f;
+    };
+    for (uint32_t g = wg;; g += 2) {
+      const int as = g % C::kNa;
+      if (!mbar_wait_warp(&aux_full[as], (g / C::kNa) & 1, err, 331)) break;
+      const TileInfo t = *info_of(g);
+      if (t.bits & kEnd) break;
+      const bool keys = t.bits & kKeys;
+      if (t.item != cur) {
+        if (grad) flush();
+        cur = t.item;
+        if (!mbar_wait_warp(&st_full[cur & 1], (cur >> 1) & 1, err, 332)) break;
+        const float* rv = row_vec(cur);
+        add = rv[r];
+        nd = keys ? 0.0f : rv[128 + r];
+        grad = want && !keys;
+        const int x = (int)(blockIdx.x + (unsigned)cur * gridDim.x) - (keys ? 0 : items);
+        const int bh = x / nr, ri = x - bh * nr;
+        row0 = ri * 128 + (warp & 3) * 32;
+        part = ((size_t)bh * a.ditems + ri * 8 + warp) * a.buckets;
+      }
+      if (!mbar_wait_warp(&s_full[wg], (g >> 1) & 1, err, 333)) break;
+      if (t.tile >= 0) {
+        tc_fence_after();
+        const uint8_t* ax = sAux + as * C::kAuxBytes;
+        const float* va = reinterpret_cast<const float*>(ax + C::kVecA);
+        const float* vb = reinterpret_cast<const float*>(ax + C::kVecB);
+        const float row = add + t.bias;
+        float far = 0.0f;
+        if (keys) {
+          if (t.bits & kNear) bwd_tile<T, true, true, false>(tS, ax, C::kWin, va, vb, c2, row, nd, r, false, far, chains, lane);
+          else bwd_tile<T, true, false, false>(tS, ax, C::kWin, va, vb, c2, row, nd, r, false, far, chains, lane);
+        } else if (t.bits & kNear) {
+          bwd_tile<T, false, true, true>(tS, ax, C::kWin, va, vb, c2, row, nd, r, grad, far, chains, lane);
+        } else if (t.bits & kMixed) {
+          bwd_tile<T, false, false, true>(tS, ax, C::kWin, va, vb, c2, row, nd, r, grad, far, chains, lane);
+        } else {
+          bwd_tile<T, false, false, false>(tS, ax, C::kWin, va, vb, c2, row, nd, r, grad, far, chains, lane);
+        }
+        if (t.bits & kAhead) far_ahead += far;
+        else far_behind += far;
+        tmem_store_wait();
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&p_full[wg]);
+        mbar_arrive(&aux_empty[as]);
+      }
+      if (grad && (t.bits & kNear)) bin_diagonals(chains, C::kChain, a.bid + a.vec_off + t.tile * 64 - row0, bins, lane);
+    }
+    if (grad) flush();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 13) tmem_dealloc(tmem, 512);
+}
+
 // ------------------------------------------------------------------ host side
 typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -621,11 +1144,32 @@ bool fwd(const AttnOp& a, cudaStream_t s) {
   return true;
 }
 
+template <typename T, int D>
+bool bwd(const AttnOp& a, cudaStream_t s) {
+  const bool bf = std::is_same<T, bf16_t>::value;
+  CUtensorMap mq, mk, mv, mdo, mdq, mdk, mdv;
+  if (!encode(&mq, a.q, a, bf, 64) || !encode(&mk, a.k, a, bf, 64) || !encode(&mv, a.v, a, bf, 64) ||
+      !encode(&mdo, a.dout, a, bf, 64) || !encode(&mdq, a.dq, a, bf, 128) || !encode(&mdk, a.dk, a, bf, 128) ||
+      !encode(&mdv, a.dv, a, bf, 128))
+    return false;
+  cudaFuncSetAttribute(attention_bwd_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Bwd<D>::kSmem);
+  const int items = a.B * a.nh * ((a.S + 127) / 128);
+  launch_pdl(attention_bwd_kernel<T, D>, std::min(2 * items, sm_count()), kBwdThreads, Bwd<D>::kSmem, s, mq, mk, mv, mdo,
+             mdq, mdk, mdv, a);
+  count_launch();
+  return true;
+}
+
 }  // namespace
 
 bool attention_tc_fwd_run(int dt, const AttnOp& a, cudaStream_t s) {
   if (dt == DT_F16) return a.d <= 64 ? fwd<half_t, 64>(a, s) : fwd<half_t, 128>(a, s);
   return a.d <= 64 ? fwd<bf16_t, 64>(a, s) : fwd<bf16_t, 128>(a, s);
+}
+
+bool attention_tc_bwd_run(int dt, const AttnOp& a, cudaStream_t s) {
+  if (dt == DT_F16) return a.d <= 64 ? bwd<half_t, 64>(a, s) : bwd<half_t, 128>(a, s);
+  return a.d <= 64 ? bwd<bf16_t, 64>(a, s) : bwd<bf16_t, 128>(a, s);
 }
 
 int attention_tc_take_error() {
