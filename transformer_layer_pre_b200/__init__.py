@@ -273,64 +273,78 @@ def _fail(what: str):
     raise TlError(1, what)
 
 
-def _on(device, stream):
-    """The stream a call is enqueued on: the current one of the tensors'
-    device, or the given one, which must be of that device."""
-    if stream is None:
-        return torch.cuda.current_stream(device)
-    if stream.device != device:
-        _fail(f"a stream of {stream.device} for tensors on {device}")
-    return stream
+class _Call:
+    """Device and stream of one call.  Without a stream, and on the current
+    device, nothing is switched (a switch costs more than a launch); else the
+    outputs are allocated on, and the call runs with, the stream's device and
+    the stream itself."""
+
+    def __init__(self, index: int, stream):
+        self.stream = stream
+        self.switch = None
+        if stream is not None:
+            if stream.device.index != index:
+                _fail(f"a stream of {stream.device} for tensors on cuda:{index}")
+            self.switch = torch.cuda.stream(stream)
+            self.raw = stream.cuda_stream
+        else:
+            if torch.cuda.current_device() != index:
+                self.switch = torch.cuda.device(index)
+            self.raw = torch._C._cuda_getCurrentRawStream(index)
+
+    def __enter__(self):
+        if self.switch is not None:
+            self.switch.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.switch is not None:
+            self.switch.__exit__(*exc)
 
 
-def _attention_call(q, k, v, mask, bias_table, max_distance, scale, others, lse):
-    """Checks shared by both attention calls; returns the description."""
-    if q.dim() != 4 or not q.is_cuda or q.dtype not in DTYPE_CODES:
+def _check(st: int) -> None:
+    if st != 0:
+        raise TlError(st, load_library().tl_status_string(st).decode())
+
+
+def _heads(name, t, shape, dtype, index):
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
+        _fail(f"{name} must have q's shape, dtype and device")
+    sb, st, sh, sd = t.stride()
+    if sd != 1:
+        _fail(f"the head_dim entries of {name} must be contiguous")
+    return _Heads(t.data_ptr(), sb, st, sh)
+
+
+def _attention_call(q, mask, bias_table, max_distance, scale, lse):
+    """Checks what both attention calls share; returns q's shape, dtype and
+    device index, and the description."""
+    shape, dtype = q.shape, q.dtype
+    code = DTYPE_CODES.get(dtype)
+    index = q.get_device()
+    if len(shape) != 4 or index < 0 or code is None:
         _fail("q must be a (batch, seq, heads, head_dim) float32, float16 or bfloat16 tensor on a CUDA device")
-    device, dtype, shape = q.device, q.dtype, q.shape
-    for name, t in (("k", k), ("v", v), *others):
-        if t.shape != shape or t.dtype != dtype or t.device != device:
-            _fail(f"{name} must have q's shape, dtype and device")
     b, s, n, d = shape
-    for name, t in (("q", q), ("k", k), ("v", v), *others):
-        if d > 1 and t.stride(3) != 1:
-            _fail(f"the head_dim entries of {name} must be contiguous")
-    desc = _Attention(DTYPE_CODES[dtype], b, s, n, d, 0.0 if scale is None else scale, None, None, 0, 0)
-    if scale is not None and not scale > 0.0:
+    if scale is None:
+        scale = 0.0
+    elif not scale > 0.0:
         _fail("scale must be positive")
+    desc = _Attention(code, b, s, n, d, scale, None, None, 0, 0)
     if mask is not None:
-        if mask.shape != (b, s) or mask.dtype != torch.float32 or mask.device != device or not mask.is_contiguous():
+        if mask.shape != (b, s) or mask.dtype is not torch.float32 or mask.get_device() != index or not mask.is_contiguous():
             _fail("mask must be a contiguous (batch, seq) float32 tensor on q's device")
         desc.mask = mask.data_ptr()
     if bias_table is not None:
-        if (bias_table.dim() != 2 or bias_table.shape[1] != n or bias_table.dtype != dtype
-                or bias_table.device != device or not bias_table.is_contiguous()):
+        if (bias_table.dim() != 2 or bias_table.shape[1] != n or bias_table.dtype is not dtype
+                or bias_table.get_device() != index or not bias_table.is_contiguous()):
             _fail("bias_table must be a contiguous (buckets, heads) tensor of q's dtype on q's device")
         desc.bias_table = bias_table.data_ptr()
         desc.buckets = bias_table.shape[0]
         desc.max_distance = max_distance
-    if lse is not None and (lse.shape != (b, n, s) or lse.dtype != torch.float32 or lse.device != device
+    if lse is not None and (lse.shape != (b, n, s) or lse.dtype is not torch.float32 or lse.get_device() != index
                             or not lse.is_contiguous()):
         _fail("lse must be a contiguous (batch, heads, seq) float32 tensor on q's device")
-    return desc
-
-
-def _heads(t):
-    sb, st, sh, _ = t.stride()
-    return _Heads(t.data_ptr(), sb, st, sh)
-
-
-def _workspace(lib, desc, backward, stream, device):
-    n = lib.tl_attention_workspace_bytes(ctypes.byref(desc), backward)
-    with torch.cuda.stream(stream):
-        return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
-
-
-def _run(fn, device, *args):
-    with torch.cuda.device(device):
-        st = fn(*args)
-    if st != 0:
-        raise TlError(st, load_library().tl_status_string(st).decode())
+    return shape, dtype, index, desc
 
 
 def attention_forward(q, k, v, mask=None, bias_table=None, max_distance=128, scale=None, o=None, lse=None,
@@ -346,16 +360,16 @@ def attention_forward(q, k, v, mask=None, bias_table=None, max_distance=128, sca
     default 1/sqrt(head_dim).  Returns (o, lse): o like q (dense unless
     given), lse (batch, heads, seq) float32, which the backward needs."""
     lib = load_library()
-    desc = _attention_call(q, k, v, mask, bias_table, max_distance, scale, (("o", o),) if o is not None else (), lse)
-    stream = _on(q.device, stream)
-    with torch.cuda.stream(stream):
+    shape, dtype, index, desc = _attention_call(q, mask, bias_table, max_distance, scale, lse)
+    hq, hk, hv = (_heads(n, t, shape, dtype, index) for n, t in (("q", q), ("k", k), ("v", v)))
+    with _Call(index, stream) as call:
         if o is None:
-            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            o = torch.empty(shape, dtype=dtype, device=q.device)
         if lse is None:
-            lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32, device=q.device)
-    ws = _workspace(lib, desc, 0, stream, q.device)
-    _run(lib.tl_attention_forward, q.device, desc, _heads(q), _heads(k), _heads(v), _heads(o), lse.data_ptr(),
-         ws.data_ptr(), ws.numel(), stream.cuda_stream)
+            lse = torch.empty((shape[0], shape[2], shape[1]), dtype=torch.float32, device=q.device)
+        ho = _heads("o", o, shape, dtype, index)
+        ws = torch.empty(lib.tl_attention_workspace_bytes(desc, 0), dtype=torch.uint8, device=q.device)
+        _check(lib.tl_attention_forward(desc, hq, hk, hv, ho, lse.data_ptr(), ws.data_ptr(), ws.numel(), call.raw))
     return o, lse
 
 
@@ -367,22 +381,27 @@ def attention_backward(q, k, v, o, lse, do, mask=None, bias_table=None, max_dist
     heads) float32, is None without a bias_table, and added to when it is
     given with accumulate=True (a table shared by several layers)."""
     lib = load_library()
-    outs = [(n, t) for n, t in (("dq", dq), ("dk", dk), ("dv", dv)) if t is not None]
-    desc = _attention_call(q, k, v, mask, bias_table, max_distance, scale, (("o", o), ("do", do), *outs), lse)
-    if dtable is not None and (bias_table is None or dtable.shape != bias_table.shape or dtable.dtype != torch.float32
-                               or dtable.device != q.device or not dtable.is_contiguous()):
-        _fail("dtable must be a contiguous float32 tensor of bias_table's shape on q's device")
-    if accumulate and dtable is None:
+    shape, dtype, index, desc = _attention_call(q, mask, bias_table, max_distance, scale, lse)
+    ins = [_heads(n, t, shape, dtype, index) for n, t in (("q", q), ("k", k), ("v", v), ("o", o), ("do", do))]
+    if dtable is not None:
+        if (bias_table is None or dtable.shape != bias_table.shape or dtable.dtype is not torch.float32
+                or dtable.get_device() != index or not dtable.is_contiguous()):
+            _fail("dtable must be a contiguous float32 tensor of bias_table's shape on q's device")
+    elif accumulate:
         _fail("accumulate needs the dtable to add to")
-    stream = _on(q.device, stream)
-    with torch.cuda.stream(stream):
-        dq, dk, dv = (torch.empty(q.shape, dtype=q.dtype, device=q.device) if t is None else t for t in (dq, dk, dv))
+    with _Call(index, stream) as call:
+        if dq is None:
+            dq = torch.empty(shape, dtype=dtype, device=q.device)
+        if dk is None:
+            dk = torch.empty(shape, dtype=dtype, device=q.device)
+        if dv is None:
+            dv = torch.empty(shape, dtype=dtype, device=q.device)
         if dtable is None and bias_table is not None:
             dtable = torch.empty(bias_table.shape, dtype=torch.float32, device=q.device)
-    ws = _workspace(lib, desc, 1, stream, q.device)
-    _run(lib.tl_attention_backward, q.device, desc, _heads(q), _heads(k), _heads(v), _heads(o), _heads(do),
-         lse.data_ptr(), _heads(dq), _heads(dk), _heads(dv), _ptr(dtable), int(accumulate), ws.data_ptr(),
-         ws.numel(), stream.cuda_stream)
+        outs = [_heads(n, t, shape, dtype, index) for n, t in (("dq", dq), ("dk", dk), ("dv", dv))]
+        ws = torch.empty(lib.tl_attention_workspace_bytes(desc, 1), dtype=torch.uint8, device=q.device)
+        _check(lib.tl_attention_backward(desc, *ins, lse.data_ptr(), *outs, _ptr(dtable), int(accumulate),
+                                         ws.data_ptr(), ws.numel(), call.raw))
     return dq, dk, dv, dtable
 
 
@@ -395,28 +414,27 @@ def clip_grad_norm(grads, max_norm, out=None, stream=None):
     lib = load_library()
     grads = list(grads)
     outs = grads if out is None else list(out)
-    if not grads or len(outs) != len(grads):
+    n = len(grads)
+    if n == 0 or len(outs) != n:
         _fail("a non-empty list of gradients, and as many outputs")
-    device, dtype = grads[0].device, grads[0].dtype
-    if device.type != "cuda" or dtype not in DTYPE_CODES:
+    dtype, index = grads[0].dtype, grads[0].get_device()
+    code = DTYPE_CODES.get(dtype)
+    if index < 0 or code is None:
         _fail("gradients must be float32, float16 or bfloat16 tensors on a CUDA device")
     for t in grads if out is None else grads + outs:
-        if t.dtype != dtype or t.device != device or not t.is_contiguous():
+        if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
             _fail("gradients and outputs must be contiguous tensors of one dtype and device")
-    n = len(grads)
     sizes = [t.numel() for t in grads]
-    src = (ctypes.c_void_p * n)(*[t.data_ptr() for t in grads])
-    dst = src
+    src = dst = (ctypes.c_void_p * n)(*[t.data_ptr() for t in grads])
     if out is not None:
         if [t.numel() for t in outs] != sizes:
             _fail("an output for every gradient, of its size")
         dst = (ctypes.c_void_p * n)(*[t.data_ptr() for t in outs])
-    stream = _on(device, stream)
-    with torch.cuda.stream(stream):
-        norm = torch.empty(1, dtype=torch.float32, device=device)
-        ws = torch.empty(lib.tl_clip_workspace_bytes(n), dtype=torch.uint8, device=device)
-    _run(lib.tl_clip_grad_norm, device, DTYPE_CODES[dtype], n, src, dst, (ctypes.c_uint64 * n)(*sizes), max_norm,
-         norm.data_ptr(), ws.data_ptr(), ws.numel(), stream.cuda_stream)
+    with _Call(index, stream) as call:
+        norm = torch.empty(1, dtype=torch.float32, device=grads[0].device)
+        ws = torch.empty(lib.tl_clip_workspace_bytes(n), dtype=torch.uint8, device=norm.device)
+        _check(lib.tl_clip_grad_norm(code, n, src, dst, (ctypes.c_uint64 * n)(*sizes), max_norm, norm.data_ptr(),
+                                     ws.data_ptr(), ws.numel(), call.raw))
     return norm
 
 

@@ -272,14 +272,16 @@ __global__ void __launch_bounds__(kThr) attn_bwd_kernel(const __grid_constant__ 
 template <int D>
 void fwd(const AttnOp& a, cudaStream_t s) {
   constexpr int smem = (3 * D + kT) * kLd * 4;
-  cudaFuncSetAttribute(attn_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> ready{0};
+  allow_smem(attn_fwd_kernel<D>, smem, ready);
   launch_pdl(attn_fwd_kernel<D>, a.B * a.nh * ((a.S + kT - 1) / kT), kThr, smem, s, a);
   count_launch();
 }
 template <int D>
 void bwd(const AttnOp& a, cudaStream_t s) {
   constexpr int smem = (4 * D + 2 * kT) * kLd * 4 + kAttnMaxBuckets * 4;
-  cudaFuncSetAttribute(attn_bwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> ready{0};
+  allow_smem(attn_bwd_kernel<D>, smem, ready);
   launch_pdl(attn_bwd_kernel<D>, 2 * a.B * a.nh * ((a.S + kT - 1) / kT), kThr, smem, s, a);
   count_launch();
 }

@@ -1123,13 +1123,6 @@ bool encode(CUtensorMap* m, const AttnView& v, const AttnOp& a, bool bf16, int r
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int sm_count() {
-  int dev = 0, n = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n;
-}
-
 template <typename T, int D>
 bool fwd(const AttnOp& a, cudaStream_t s) {
   const bool bf = std::is_same<T, bf16_t>::value;
@@ -1137,7 +1130,8 @@ bool fwd(const AttnOp& a, cudaStream_t s) {
   if (!encode(&mq, a.q, a, bf, 128) || !encode(&mk, a.k, a, bf, Fwd<D>::kTK) ||
       !encode(&mv, a.v, a, bf, Fwd<D>::kTK) || !encode(&mo, a.o, a, bf, 128))
     return false;
-  cudaFuncSetAttribute(attention_fwd_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Fwd<D>::kSmem);
+  static std::atomic<uint64_t> ready{0};
+  allow_smem(attention_fwd_kernel<T, D>, Fwd<D>::kSmem, ready);
   const int items = a.B * a.nh * ((a.S + 127) / 128);
   launch_pdl(attention_fwd_kernel<T, D>, std::min(items, Fwd<D>::kBlocks * sm_count()), kFwdThreads, Fwd<D>::kSmem, s, mq, mk, mv, mo, a);
   count_launch();
@@ -1152,7 +1146,8 @@ bool bwd(const AttnOp& a, cudaStream_t s) {
       !encode(&mdo, a.dout, a, bf, 64) || !encode(&mdq, a.dq, a, bf, 128) || !encode(&mdk, a.dk, a, bf, 128) ||
       !encode(&mdv, a.dv, a, bf, 128))
     return false;
-  cudaFuncSetAttribute(attention_bwd_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Bwd<D>::kSmem);
+  static std::atomic<uint64_t> ready{0};
+  allow_smem(attention_bwd_kernel<T, D>, Bwd<D>::kSmem, ready);
   const int items = a.B * a.nh * ((a.S + 127) / 128);
   launch_pdl(attention_bwd_kernel<T, D>, std::min(2 * items, sm_count()), kBwdThreads, Bwd<D>::kSmem, s, mq, mk, mv, mdo,
              mdq, mdk, mdv, a);

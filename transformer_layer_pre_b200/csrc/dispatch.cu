@@ -11,6 +11,16 @@ int gemm_tc_run2(int dtype, const GemmDesc& ga, const EpiParams& ea, const GemmD
 size_t gemm_tc_splitk_ws_floats(int M, int N, int K);
 int gemm_tc_take_error();
 
+int sm_count() {
+  static std::atomic<int> known[64];
+  int dev = 0, n = 0;
+  cudaGetDevice(&dev);
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed))) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 int gemm_uses_tensor_cores(int dtype) { return dtype != DT_F32; }
 
 int gemm_run(int dtype, const GemmDesc& g, const EpiParams& e, cudaStream_t s) {

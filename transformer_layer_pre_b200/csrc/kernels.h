@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace tlp {
@@ -28,6 +30,20 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
+// Raises a kernel's dynamic shared memory limit, once per device (the calls
+// after the first cost an atomic load).  `done`: a static of the caller's, one
+// per kernel.
+template <typename K>
+inline void allow_smem(K* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess)
+    done.fetch_or(bit, std::memory_order_release);
+}
+// SMs of the current device.
+int sm_count();
 inline size_t dtype_size(int dt) { return dt == DT_F32 ? 4 : 2; }
 
 // ------------------------------------------------------------------ GEMM
