@@ -364,11 +364,11 @@ def attention_forward(q, k, v, mask=None, bias_table=None, max_distance=128, sca
     hq, hk, hv = (_heads(n, t, shape, dtype, index) for n, t in (("q", q), ("k", k), ("v", v)))
     with _Call(index, stream) as call:
         if o is None:
-            o = torch.empty(shape, dtype=dtype, device=q.device)
+            o = q.new_empty(shape)
         if lse is None:
-            lse = torch.empty((shape[0], shape[2], shape[1]), dtype=torch.float32, device=q.device)
+            lse = q.new_empty((shape[0], shape[2], shape[1]), dtype=torch.float32)
         ho = _heads("o", o, shape, dtype, index)
-        ws = torch.empty(lib.tl_attention_workspace_bytes(desc, 0), dtype=torch.uint8, device=q.device)
+        ws = q.new_empty(max(1, lib.tl_attention_workspace_bytes(desc, 0)), dtype=torch.uint8)
         _check(lib.tl_attention_forward(desc, hq, hk, hv, ho, lse.data_ptr(), ws.data_ptr(), ws.numel(), call.raw))
     return o, lse
 
@@ -391,15 +391,15 @@ def attention_backward(q, k, v, o, lse, do, mask=None, bias_table=None, max_dist
         _fail("accumulate needs the dtable to add to")
     with _Call(index, stream) as call:
         if dq is None:
-            dq = torch.empty(shape, dtype=dtype, device=q.device)
+            dq = q.new_empty(shape)
         if dk is None:
-            dk = torch.empty(shape, dtype=dtype, device=q.device)
+            dk = q.new_empty(shape)
         if dv is None:
-            dv = torch.empty(shape, dtype=dtype, device=q.device)
+            dv = q.new_empty(shape)
         if dtable is None and bias_table is not None:
-            dtable = torch.empty(bias_table.shape, dtype=torch.float32, device=q.device)
+            dtable = q.new_empty(bias_table.shape, dtype=torch.float32)
         outs = [_heads(n, t, shape, dtype, index) for n, t in (("dq", dq), ("dk", dk), ("dv", dv))]
-        ws = torch.empty(lib.tl_attention_workspace_bytes(desc, 1), dtype=torch.uint8, device=q.device)
+        ws = q.new_empty(max(1, lib.tl_attention_workspace_bytes(desc, 1)), dtype=torch.uint8)
         _check(lib.tl_attention_backward(desc, *ins, lse.data_ptr(), *outs, _ptr(dtable), int(accumulate),
                                          ws.data_ptr(), ws.numel(), call.raw))
     return dq, dk, dv, dtable
@@ -421,18 +421,19 @@ def clip_grad_norm(grads, max_norm, out=None, stream=None):
     code = DTYPE_CODES.get(dtype)
     if index < 0 or code is None:
         _fail("gradients must be float32, float16 or bfloat16 tensors on a CUDA device")
-    for t in grads if out is None else grads + outs:
-        if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
-            _fail("gradients and outputs must be contiguous tensors of one dtype and device")
-    sizes = [t.numel() for t in grads]
-    src = dst = (ctypes.c_void_p * n)(*[t.data_ptr() for t in grads])
+    every = grads if out is None else grads + outs
+    if (any([t.dtype is not dtype for t in every]) or set(map(torch.Tensor.get_device, every)) != {index}
+            or not all(map(torch.Tensor.is_contiguous, every))):
+        _fail("gradients and outputs must be contiguous tensors of one dtype and device")
+    sizes = list(map(torch.Tensor.numel, grads))
+    src = dst = (ctypes.c_void_p * n)(*map(torch.Tensor.data_ptr, grads))
     if out is not None:
-        if [t.numel() for t in outs] != sizes:
+        if list(map(torch.Tensor.numel, outs)) != sizes:
             _fail("an output for every gradient, of its size")
-        dst = (ctypes.c_void_p * n)(*[t.data_ptr() for t in outs])
+        dst = (ctypes.c_void_p * n)(*map(torch.Tensor.data_ptr, outs))
     with _Call(index, stream) as call:
-        norm = torch.empty(1, dtype=torch.float32, device=grads[0].device)
-        ws = torch.empty(lib.tl_clip_workspace_bytes(n), dtype=torch.uint8, device=norm.device)
+        norm = grads[0].new_empty(1, dtype=torch.float32)
+        ws = norm.new_empty(lib.tl_clip_workspace_bytes(n), dtype=torch.uint8)
         _check(lib.tl_clip_grad_norm(code, n, src, dst, (ctypes.c_uint64 * n)(*sizes), max_norm, norm.data_ptr(),
                                      ws.data_ptr(), ws.numel(), call.raw))
     return norm
