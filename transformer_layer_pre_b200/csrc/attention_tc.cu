@@ -54,6 +54,26 @@ template <> __device__ __forceinline__ uint32_t pack2<bf16_t>(float lo, float hi
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Bounded wait on an mbarrier that pauses between its polls: polls go through
+// the shared memory that the products read their operands from (a tight loop
+// of polls in every waiting warp made the backward 14 % slower).
+template <int NS>
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, int* err, int code) {
+  if (mbar_try_wait(bar, parity)) return true;
+  if (NS > 0) {
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i) {
+      __nanosleep(NS);
+      if (mbar_try_wait(bar, parity)) return true;
+    }
+  }
+  return mbar_wait(bar, parity, err, code);
+}
+// The same by a whole warp, whose lanes go on together.
+template <int NS>
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* err, int code) {
+  return __all_sync(0xffffffffu, wait_bar<NS>(bar, parity, err, code)) != 0;
+}
 // 32 TMEM columns, no wait (the caller waits once for several).
 __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, float* r) {
   asm volatile(
@@ -262,7 +282,7 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
       const float* vec = a.vec ? bias_copy(a, h, 0, 0) : nullptr;
       const float behind = vec ? vec[a.vec_off - a.sat] : 0.0f, ahead = vec ? vec[a.vec_off + a.sat] : 0.0f;
       if (lane == 0) {
-        ok = mbar_wait(q_empty, (n & 1) ^ 1, err, 201);
+        ok = wait_bar<0>(q_empty, (n & 1) ^ 1, err, 201);
         if (ok) {
           ++nq_issued;
           mbar_arrive_expect_tx(q_full, C::kQBytes);
@@ -294,7 +314,7 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
               else near = true;
             }
             const int ks = kc % C::kKv;
-            if ((ok = mbar_wait(&k_empty[ks], ((kc / C::kKv) & 1) ^ 1, err, 202))) {
+            if ((ok = wait_bar<0>(&k_empty[ks], ((kc / C::kKv) & 1) ^ 1, err, 202))) {
               ++nk_issued;
               mbar_arrive_expect_tx(&k_full[ks], C::kKvBytes);
               for (int c = 0; c < D / 64; ++c)
@@ -302,7 +322,7 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
             }
           }
           if (near) t.bits |= kNear;
-          if (ok && (ok = mbar_wait(&aux_empty[as], ((g / C::kAux) & 1) ^ 1, err, 203))) {
+          if (ok && (ok = wait_bar<0>(&aux_empty[as], ((g / C::kAux) & 1) ^ 1, err, 203))) {
             uint8_t* ax = sAux + as * C::kAuxBytes;
             *info_of(g) = t;
             const bool mk = !none && mix;
@@ -316,7 +336,7 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
           }
           if (ok && !none) {
             const int ks = kc % C::kKv;
-            if ((ok = mbar_wait(&v_empty[ks], ((kc / C::kKv) & 1) ^ 1, err, 204))) {
+            if ((ok = wait_bar<0>(&v_empty[ks], ((kc / C::kKv) & 1) ^ 1, err, 204))) {
               ++nv_issued;
               mbar_arrive_expect_tx(&v_full[ks], C::kKvBytes);
               for (int c = 0; c < D / 64; ++c)
@@ -354,19 +374,19 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
       TileInfo t;
       auto next_info = [&](uint32_t e) -> bool {
         const int as = e % C::kAux;
-        if (!mbar_wait(&aux_full[as], (e / C::kAux) & 1, err, 213)) return false;
+        if (!wait_bar<0>(&aux_full[as], (e / C::kAux) & 1, err, 213)) return false;
         t = *info_of(e);
         mbar_arrive(&aux_empty[as]);
-        return t.tile < 0 || mbar_wait(&k_full[kc % C::kKv], (kc / C::kKv) & 1, err, 216);
+        return t.tile < 0 || wait_bar<0>(&k_full[kc % C::kKv], (kc / C::kKv) & 1, err, 216);
       };
       for (int it = blockIdx.x; it < nitems && ok; it += gridDim.x, ++n) {
-        if (!(ok = next_info(g)) || !(ok = mbar_wait(q_full, n & 1, err, 214))) break;
+        if (!(ok = next_info(g)) || !(ok = wait_bar<0>(q_full, n & 1, err, 214))) break;
         for (;; ++g) {
           const bool last = t.bits & kLast, first = t.bits & kFirst;
           if (t.tile < 0) {
             // nothing to multiply: the phases go on
             mbar_arrive(s_full);
-            if (!(ok = mbar_wait(p_full, g & 1, err, 211))) break;
+            if (!(ok = wait_bar<0>(p_full, g & 1, err, 211))) break;
             mbar_arrive(pv_done);
             break;
           }
@@ -383,9 +403,9 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
           // what the next tile needs, ahead of the wait for P (an item's first
           // tile waits for the rows of the item before)
           if (!last && !(ok = next_info(g + 1))) break;
-          if (!(ok = mbar_wait(&v_full[ks], kp, err, 212))) break;
+          if (!(ok = wait_bar<0>(&v_full[ks], kp, err, 212))) break;
           // P lies over S, so its product comes before the next Q K^T
-          if (!(ok = mbar_wait(p_full, g & 1, err, 211))) break;
+          if (!(ok = wait_bar<0>(p_full, g & 1, err, 211))) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < C::kTK / 16; ++kk)
@@ -412,10 +432,10 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
       bool last = false;
       for (; !last; ++g) {
         const int as = g % C::kAux;
-        if (!(ok = mbar_wait_warp(&aux_full[as], (g / C::kAux) & 1, err, 221))) break;
+        if (!(ok = wait_warp<0>(&aux_full[as], (g / C::kAux) & 1, err, 221))) break;
         const TileInfo t = *info_of(g);
         last = t.bits & kLast;
-        if (!(ok = mbar_wait_warp(s_full, g & 1, err, 222))) break;
+        if (!(ok = wait_warp<0>(s_full, g & 1, err, 222))) break;
         if (t.tile < 0) {
           __syncwarp();
           if (lane == 0) {
@@ -525,7 +545,7 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
       }
       if (!ok) break;
       // ---- the item's rows: O / l through the Q tile (no product reads it any more)
-      if (!(ok = mbar_wait_warp(pv_done, n & 1, err, 225))) break;
+      if (!(ok = wait_warp<0>(pv_done, n & 1, err, 225))) break;
       tc_fence_after();
       uint8_t* stage = sQ;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -581,30 +601,41 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
 //
 // Warps 0-3 and 4-7 take the moving tiles in turn (one row, that is one TMEM
 // lane, per thread), so one tile's exponentials run while the other's
-// products do; 8-11 write the finished rows out; 12: TMA; 13: MMA.  P and dS
+// products do; 8-11 write the finished rows out; 12: TMA; 13 issues S and dP,
+// 14 the sums (one thread for both spent its time in waits of the one that the
+// other did not need).  P and dS
 // (rounded to the storage type, at most half a step) overwrite S and dP in
 // TMEM and are the A operands of the second pair of products from there, so
 // they never touch shared memory.
 // TMEM: per softmax group S, dP (64 columns each); from 256 on the sums, two
 // sets of them for D = 64, so the next item starts while one is written out.
-template <int D>
+constexpr int kRun = 192, kWin = 200;           // diagonals of a 128 x 64 tile, floats of a window copy
+constexpr int kVecs = 4 * kWin * 4;             // column vectors after the four copies
+constexpr int kChain = 48;                      // floats of a diagonal chain
+template <int D, bool LONG>
 struct Bwd {
   static constexpr int kSt = D / 64 * kRegion;                      // a stationary tile
   static constexpr int kMvRegion = 64 * 128;
   static constexpr int kMv = D / 64 * kMvRegion;                    // a moving tile
-  static constexpr int kNs = D == 64 ? 4 : 2;                       // moving stages
-  static constexpr int kNa = 4;                                     // tile descriptions
+  static constexpr int kSlots = D == 128 && LONG ? 1 : 2;           // stationary pairs
+  static constexpr int kNs = D == 64 || LONG ? 4 : 2;               // moving pairs
+  static constexpr int kBuf = 2;                                    // S, dP buffers
   static constexpr int kAcc = D == 64 ? 2 : 1;                      // sets of sums
-  static constexpr int kRun = 192, kWin = 200;
-  static constexpr int kVecA = 4 * kWin * 4, kVecB = kVecA + 256, kInfo = kVecB + 256;
-  static constexpr int kAuxBytes = kInfo + 16;
+  static constexpr uint32_t kSums = kBuf * 128;                     // their first TMEM column
+  static constexpr int kNa = D == 64 ? 6 : 4;                       // tile descriptions
+  static constexpr int kAuxBytes = kVecs + 512 + 16;
   static constexpr int kStAux = 2 * 128 * 4 + 16;                   // row vectors, empty flag
-  static constexpr int kChain = 48;                                 // floats of a diagonal chain, see bias_diagonals
-  static constexpr int kSmem = 4 * kSt + 2 * kNs * kMv + kNa * kAuxBytes + 2 * kStAux + 8 * kAttnMaxBuckets * 4 +
-                               8 * 4 * kChain * 4 + 320;
+  static constexpr int kSmem = kSlots * 2 * kSt + 2 * kNs * kMv + kNa * kAuxBytes + kSlots * kStAux +
+                               8 * kAttnMaxBuckets * 4 + 8 * 4 * kChain * 4 + 400;
+  static_assert(kSums + kAcc * 2 * D <= 512, "the sums do not fit the tensor memory");
+  static_assert(kSmem <= 227 * 1024, "the backward's shared memory exceeds a block's maximum");
 };
-static_assert(Bwd<128>::kSmem <= 227 * 1024, "the backward's shared memory exceeds a block's maximum");
-constexpr int kBwdThreads = 448;
+// D = 128 from this length on: one stationary pair and four moving ones instead
+// of two and two (shared memory holds six).  B4 h8 S2048: 310 us against 344;
+// B8 h8 S512, whose items are short: 84 against 82.
+constexpr int kLongSeq = 1024;
+constexpr int kBwdThreads = 480;
+constexpr int kPauseLoad = 50, kPauseSoft = 20, kPauseStore = 200;   // ns between polls
 
 // Sums the diagonals of a warp's 32 rows x 16 columns (v: this lane's row).
 // Diagonal t - lane moves up one lane per column, so the running sums are
@@ -714,43 +745,42 @@ __device__ __forceinline__ void bwd_tile(uint32_t tS, const uint8_t* ax, int win
     if (KEYS) tmem_st16u(tS + c * 16, wp);
     tmem_st16u(tS + 64 + c * 16, wd);
     if (!KEYS && NEAR && grad) {
-      diagonal_chain(dp, chains + (2 * c) * Bwd<64>::kChain, lane);
-      diagonal_chain(dp + 16, chains + (2 * c + 1) * Bwd<64>::kChain, lane);
+      diagonal_chain(dp, chains + (2 * c) * kChain, lane);
+      diagonal_chain(dp + 16, chains + (2 * c + 1) * kChain, lane);
     }
   }
   far_sum += fs.x + fs.y;
 }
 
-template <typename T, int D>
+template <typename T, int D, bool LONG>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     attention_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                          const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
                          const __grid_constant__ CUtensorMap tdq, const __grid_constant__ CUtensorMap tdk,
                          const __grid_constant__ CUtensorMap tdv, const __grid_constant__ AttnOp a) {
-  using C = Bwd<D>;
+  using C = Bwd<D, LONG>;
   // the only shared memory of the kernel: its start is 1024-byte aligned
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* sSt = smem_raw;                                  // [2] x (A1, A2)
-  uint8_t* sMv = sSt + 4 * C::kSt;                          // [kNs] x (B1, B2)
+  uint8_t* sSt = smem_raw;                                  // [kSlots] x (A1, A2)
+  uint8_t* sMv = sSt + C::kSlots * 2 * C::kSt;                          // [kNs] x (B1, B2)
   uint8_t* sAux = sMv + 2 * C::kNs * C::kMv;                // [kNa]
   uint8_t* sStAux = sAux + C::kNa * C::kAuxBytes;           // [2]
-  float* sBins = reinterpret_cast<float*>(sStAux + 2 * C::kStAux);
+  float* sBins = reinterpret_cast<float*>(sStAux + C::kSlots * C::kStAux);
   float* sChains = sBins + 8 * kAttnMaxBuckets;
-  uint64_t* bar = reinterpret_cast<uint64_t*>(sChains + 8 * 4 * C::kChain);
-  uint64_t *st_full = bar, *st_empty = st_full + 2, *mv_full = st_empty + 2, *mv_empty = mv_full + C::kNs,
-           *aux_full = mv_empty + C::kNs, *aux_empty = aux_full + C::kNa, *s_full = aux_empty + C::kNa,
-           *p_full = s_full + 2, *acc_full = p_full + 2, *acc_free = acc_full + C::kAcc;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sChains + 8 * 4 * kChain);
+  uint64_t *st_full = bar, *st_empty = st_full + C::kSlots, *mv_full = st_empty + C::kSlots,
+           *mv_empty = mv_full + C::kNs, *aux_full = mv_empty + C::kNs, *aux_empty = aux_full + C::kNa,
+           *s_full = aux_empty + C::kNa, *p_full = s_full + C::kBuf, *s_free = p_full + C::kBuf,
+           *acc_full = s_free + C::kBuf, *acc_free = acc_full + C::kAcc;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(acc_free + C::kAcc);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* err = g_attention_err;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&st_full[i], 1), mbar_init(&st_empty[i], 1);
-      mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 4);
-    }
+    for (int i = 0; i < C::kSlots; ++i) mbar_init(&st_full[i], 1), mbar_init(&st_empty[i], 1);
+    for (int i = 0; i < C::kBuf; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 4), mbar_init(&s_free[i], 1);
     for (int i = 0; i < C::kNs; ++i) mbar_init(&mv_full[i], 1), mbar_init(&mv_empty[i], 1);
-    for (int i = 0; i < C::kNa; ++i) mbar_init(&aux_full[i], 1), mbar_init(&aux_empty[i], 5);
+    for (int i = 0; i < C::kNa; ++i) mbar_init(&aux_full[i], 1), mbar_init(&aux_empty[i], 6);
     for (int i = 0; i < C::kAcc; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_free[i], 4);
     fence_barrier_init();
   }
@@ -765,10 +795,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int nr = (a.S + 127) / 128, nm = (a.S + 63) / 64;
   const int items = a.B * a.nh * nr;
   auto info_of = [&](uint32_t g) -> TileInfo* {
-    return reinterpret_cast<TileInfo*>(sAux + (g % C::kNa) * C::kAuxBytes + C::kInfo);
+    return reinterpret_cast<TileInfo*>(sAux + (g % C::kNa) * C::kAuxBytes + kVecs + 512);
   };
-  auto row_vec = [&](int n) { return reinterpret_cast<float*>(sStAux + (n & 1) * C::kStAux); };
-  auto none_flag = [&](int n) { return reinterpret_cast<int*>(sStAux + (n & 1) * C::kStAux + 1024); };
+  auto row_vec = [&](int n) { return reinterpret_cast<float*>(sStAux + (n % C::kSlots) * C::kStAux); };
+  auto none_flag = [&](int n) { return reinterpret_cast<int*>(sStAux + (n % C::kSlots) * C::kStAux + 1024); };
 
   if (warp == 12) {
     // ---- producer
@@ -787,8 +817,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       bool mix = false;
       int j = keys ? (flags[2 * ri] == 2 && flags[2 * ri + 1] == 2 ? nm : 0) : tiles.next(0, mix);
       const bool none = j == nm;
-      const int slot = n & 1;
-      if (lane == 0 && (ok = mbar_wait(&st_empty[slot], ((n >> 1) & 1) ^ 1, err, 301))) {
+      const int slot = n % C::kSlots;
+      if (lane == 0 && (ok = wait_bar<kPauseLoad>(&st_empty[slot], ((n / C::kSlots) & 1) ^ 1, err, 301))) {
         *none_flag(n) = none;
         ++st_issued;
         mbar_arrive_expect_tx(&st_full[slot], 2 * C::kSt + (keys ? 512 : 1024));
@@ -830,26 +860,26 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
             if (mix && !keys) t.bits |= kMixed;
           }
-          if ((ok = mbar_wait(&aux_empty[as], ((g / C::kNa) & 1) ^ 1, err, 302))) {
+          if ((ok = wait_bar<kPauseLoad>(&aux_empty[as], ((g / C::kNa) & 1) ^ 1, err, 302))) {
             uint8_t* ax = sAux + as * C::kAuxBytes;
             *info_of(g) = t;
             const bool near = t.bits & kNear, va = !none && (keys || near || (t.bits & kMixed));
             ++aux_issued;
-            mbar_arrive_expect_tx(&aux_full[as], (near ? 4 * C::kRun * 4 : 0) + (va ? 256 : 0) + (keys && !none ? 256 : 0));
+            mbar_arrive_expect_tx(&aux_full[as], (near ? 4 * kRun * 4 : 0) + (va ? 256 : 0) + (keys && !none ? 256 : 0));
             if (near)
               for (int s = 0; s < 4; ++s)
-                bulk_load_1d(ax + s * C::kWin * 4, bias_copy(a, h, keys ? 1 : 0, s) + x0 - 128 + a.vec_off, C::kRun * 4,
+                bulk_load_1d(ax + s * kWin * 4, bias_copy(a, h, keys ? 1 : 0, s) + x0 - 128 + a.vec_off, kRun * 4,
                              &aux_full[as]);
             if (va)
-              bulk_load_1d(ax + C::kVecA,
+              bulk_load_1d(ax + kVecs,
                            (keys ? a.stats + (size_t)bh * 2 * a.Sp : a.maskx + (size_t)mb * a.Sp) + j * 64, 256,
                            &aux_full[as]);
             if (keys && !none)
-              bulk_load_1d(ax + C::kVecB, a.stats + (size_t)bh * 2 * a.Sp + a.Sp + j * 64, 256, &aux_full[as]);
+              bulk_load_1d(ax + kVecs + 256, a.stats + (size_t)bh * 2 * a.Sp + a.Sp + j * 64, 256, &aux_full[as]);
           }
           if (ok && !none) {
             const int ms = mc % C::kNs;
-            if ((ok = mbar_wait(&mv_empty[ms], ((mc / C::kNs) & 1) ^ 1, err, 303))) {
+            if ((ok = wait_bar<kPauseLoad>(&mv_empty[ms], ((mc / C::kNs) & 1) ^ 1, err, 303))) {
               ++mv_issued;
               mbar_arrive_expect_tx(&mv_full[ms], 2 * C::kMv);
               uint8_t* mv = sMv + ms * 2 * C::kMv;
@@ -868,88 +898,93 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         mix = nmix;
       } while (ok && j < nm);
     }
-    // the end, for either softmax group (the MMA thread stops at the first)
+    // the end, for either softmax group (the issuing threads stop at the first)
     for (int e = 0; e < 2 && ok && lane == 0; ++e, ++g) {
-      if (!(ok = mbar_wait(&aux_empty[g % C::kNa], ((g / C::kNa) & 1) ^ 1, err, 304))) break;
+      if (!(ok = wait_bar<kPauseLoad>(&aux_empty[g % C::kNa], ((g / C::kNa) & 1) ^ 1, err, 304))) break;
       TileInfo t = {-1, kEnd, 0.0f, -1};
       *info_of(g) = t;
       ++aux_issued;
       mbar_arrive(&aux_full[g % C::kNa]);
     }
     if (!ok && lane == 0) {
-      drain<2>(st_full, st_issued);
+      drain<C::kSlots>(st_full, st_issued);
       drain<C::kNs>(mv_full, mv_issued);
       drain<C::kNa>(aux_full, aux_issued);
     }
   } else if (warp == 13) {
+    // ---- S and dP of each tile, as soon as its operands and a buffer are there
     if (lane == 0) {
-      const bool bf = std::is_same<T, bf16_t>::value;
-      const uint32_t id_s = idesc_f16(128, 64, bf, false, false);
-      const uint32_t id_a = idesc_f16(128, D, bf, false, true);
-      const uint64_t dst = desc_k(smem_u32(sSt), 0, kRegion), dmv = desc_k(smem_u32(sMv), 0, C::kMvRegion),
-                     dmn = desc_mn(smem_u32(sMv), 0, C::kMvRegion);
-      uint32_t g = 0, mc = 0;
-      bool ok = true, pending = false;
-      TileInfo p = {-1, 0, 0.0f, 0};   // the tile whose second products are not issued yet
-      uint32_t p_g = 0, p_mc = 0;
-      auto sums = [&]() -> bool {
-        const int w = p_g & 1, ab = p.item % C::kAcc;
-        if (!mbar_wait(&p_full[w], (p_g >> 1) & 1, err, 311)) return false;
-        if ((p.bits & kFirst) && !mbar_wait(&acc_free[ab], ((p.item / C::kAcc) & 1) ^ 1, err, 312)) return false;
-        if (p.tile < 0) {
-          mbar_arrive(&acc_full[ab]);
-          return true;
-        }
-        tc_fence_after();
-        const int ms = p_mc % C::kNs;
-        const uint32_t acc1 = tmem + 256 + ab * 2 * D, acc2 = acc1 + D, tS = tmem + w * 128;
-        const uint64_t b1 = dmn + ms * (2 * C::kMv >> 4), b2 = b1 + (C::kMv >> 4);
-        const uint32_t more = p.bits & kFirst ? 0u : 1u;
-        if (p.bits & kKeys) {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma_f16_ts(acc2, tS + kk * 8, b2 + kk * 128, id_a, more | (kk > 0));
-        }
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) mma_f16_ts(acc1, tS + 64 + kk * 8, b1 + kk * 128, id_a, more | (kk > 0));
-        mma_commit(&mv_empty[ms]);
-        if (p.bits & kLast) mma_commit(&acc_full[ab]);
-        return true;
-      };
-      for (;; ++g) {
-        const int as = g % C::kNa, w = g & 1;
-        if (!(ok = mbar_wait(&aux_full[as], (g / C::kNa) & 1, err, 313))) break;
+      const uint32_t id = idesc_f16(128, 64, std::is_same<T, bf16_t>::value, false, false);
+      const uint64_t dst = desc_k(smem_u32(sSt), 0, kRegion), dmv = desc_k(smem_u32(sMv), 0, C::kMvRegion);
+      uint32_t mc = 0;
+      for (uint32_t g = 0;; ++g) {
+        const int as = g % C::kNa, w = g % C::kBuf;
+        if (!wait_bar<0>(&aux_full[as], (g / C::kNa) & 1, err, 313)) break;
         const TileInfo t = *info_of(g);
         mbar_arrive(&aux_empty[as]);
         if (t.bits & kEnd) break;
-        const int slot = t.item & 1;
-        if ((t.bits & kFirst) && !(ok = mbar_wait(&st_full[slot], (t.item >> 1) & 1, err, 314))) break;
+        const int slot = t.item % C::kSlots;
+        if ((t.bits & kFirst) && !wait_bar<0>(&st_full[slot], (t.item / C::kSlots) & 1, err, 314)) break;
+        // the buffer's last tile has been multiplied out of it
+        if (!wait_bar<0>(&s_free[w], ((g / C::kBuf) & 1) ^ 1, err, 316)) break;
         if (t.tile < 0) {
           mbar_arrive(&s_full[w]);
-        } else {
-          const int ms = mc % C::kNs;
-          if (!(ok = mbar_wait(&mv_full[ms], (mc / C::kNs) & 1, err, 315))) break;
-          tc_fence_after();
-          const uint64_t a1 = dst + slot * (2 * C::kSt >> 4), a2 = a1 + (C::kSt >> 4);
-          const uint64_t b1 = dmv + ms * (2 * C::kMv >> 4), b2 = b1 + (C::kMv >> 4);
-          const uint32_t tS = tmem + w * 128;
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_f16(tS, a1 + (kk >> 2) * (kRegion >> 4) + (kk & 3) * 2, b1 + (kk >> 2) * (C::kMvRegion >> 4) + (kk & 3) * 2,
-                    id_s, kk > 0);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_f16(tS + 64, a2 + (kk >> 2) * (kRegion >> 4) + (kk & 3) * 2,
-                    b2 + (kk >> 2) * (C::kMvRegion >> 4) + (kk & 3) * 2, id_s, kk > 0);
-          mma_commit(&s_full[w]);
+          continue;
         }
-        if (pending && !(ok = sums())) break;
-        pending = true;
-        p = t;
-        p_g = g;
-        p_mc = mc;
-        if (t.tile >= 0) ++mc;
+        const int ms = mc % C::kNs;
+        if (!wait_bar<0>(&mv_full[ms], (mc / C::kNs) & 1, err, 315)) break;
+        ++mc;
+        tc_fence_after();
+        const uint64_t a1 = dst + slot * (2 * C::kSt >> 4), a2 = a1 + (C::kSt >> 4);
+        const uint64_t b1 = dmv + ms * (2 * C::kMv >> 4), b2 = b1 + (C::kMv >> 4);
+        const uint32_t tS = tmem + w * 128;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_f16(tS, a1 + (kk >> 2) * (kRegion >> 4) + (kk & 3) * 2, b1 + (kk >> 2) * (C::kMvRegion >> 4) + (kk & 3) * 2,
+                  id, kk > 0);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_f16(tS + 64, a2 + (kk >> 2) * (kRegion >> 4) + (kk & 3) * 2,
+                  b2 + (kk >> 2) * (C::kMvRegion >> 4) + (kk & 3) * 2, id, kk > 0);
+        mma_commit(&s_full[w]);
       }
-      if (ok && pending) sums();
+    }
+  } else if (warp == 14) {
+    // ---- the sums, as soon as a tile's P and dS are there
+    if (lane == 0) {
+      const uint32_t id = idesc_f16(128, D, std::is_same<T, bf16_t>::value, false, true);
+      const uint64_t dmn = desc_mn(smem_u32(sMv), 0, C::kMvRegion);
+      uint32_t mc = 0;
+      for (uint32_t g = 0;; ++g) {
+        const int as = g % C::kNa, w = g % C::kBuf;
+        if (!wait_bar<0>(&aux_full[as], (g / C::kNa) & 1, err, 317)) break;
+        const TileInfo t = *info_of(g);
+        mbar_arrive(&aux_empty[as]);
+        if (t.bits & kEnd) break;
+        const int ab = t.item % C::kAcc;
+        if ((t.bits & kFirst) && !wait_bar<0>(&acc_free[ab], ((t.item / C::kAcc) & 1) ^ 1, err, 312)) break;
+        if (!wait_bar<0>(&p_full[w], (g / C::kBuf) & 1, err, 311)) break;
+        if (t.tile < 0) {
+          mbar_arrive(&s_free[w]);
+          mbar_arrive(&acc_full[ab]);
+          continue;
+        }
+        tc_fence_after();
+        const int ms = mc % C::kNs;
+        ++mc;
+        const uint32_t acc1 = tmem + C::kSums + ab * 2 * D, acc2 = acc1 + D, tS = tmem + w * 128;
+        const uint64_t b1 = dmn + ms * (2 * C::kMv >> 4), b2 = b1 + (C::kMv >> 4);
+        const uint32_t more = t.bits & kFirst ? 0u : 1u;
+        if (t.bits & kKeys) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) mma_f16_ts(acc2, tS + kk * 8, b2 + kk * 128, id, more | (kk > 0));
+        }
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) mma_f16_ts(acc1, tS + 64 + kk * 8, b1 + kk * 128, id, more | (kk > 0));
+        mma_commit(&s_free[w]);
+        mma_commit(&mv_empty[ms]);
+        if (t.bits & kLast) mma_commit(&acc_full[ab]);
+      }
     }
   } else if (warp >= 8) {
     // ---- finished rows: TMEM -> scale -> the item's own stationary tiles (no
@@ -961,10 +996,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     for (int it = blockIdx.x; it < 2 * items && ok; it += gridDim.x, ++n) {
       const bool keys = it < items;
       const int x = keys ? it : it - items, bh = x / nr, ri = x - bh * nr, b = bh / a.nh, h = bh - b * a.nh;
-      const int slot = n & 1, ab = n % C::kAcc;
-      if (!(ok = mbar_wait_warp(&st_full[slot], (n >> 1) & 1, err, 321))) break;
+      const int slot = n % C::kSlots, ab = n % C::kAcc;
+      if (!(ok = wait_warp<kPauseStore>(&st_full[slot], (n / C::kSlots) & 1, err, 321))) break;
       const bool none = *none_flag(n) != 0;
-      if (!(ok = mbar_wait_warp(&acc_full[ab], (n / C::kAcc) & 1, err, 322))) break;
+      if (!(ok = wait_warp<kPauseStore>(&acc_full[ab], (n / C::kAcc) & 1, err, 322))) break;
       tc_fence_after();
       uint8_t* st = sSt + slot * 2 * C::kSt;
 #pragma unroll 1
@@ -974,7 +1009,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           float v[32];
-          tmem_ld32_nowait(tmem + lo + 256 + ab * 2 * D + q * D + c * 32, v);
+          tmem_ld32_nowait(tmem + lo + C::kSums + ab * 2 * D + q * D + c * 32, v);
           tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -1009,10 +1044,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // ---- softmax groups
     const int wg = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
-    const uint32_t tS = tmem + wg * 128 + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t lo = (uint32_t)((warp & 3) * 32) << 16;
     const float c2 = a.c2;
     float* bins = sBins + warp * kAttnMaxBuckets;
-    float* chains = sChains + warp * 4 * C::kChain;
+    float* chains = sChains + warp * 4 * kChain;
     const bool want = a.dpart != nullptr;
     if (want)
       for (int u = lane; u < a.buckets; u += 32) bins[u] = 0.0f;
@@ -1037,15 +1072,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       far_behind = far_ahead = 0.0f;
     };
     for (uint32_t g = wg;; g += 2) {
-      const int as = g % C::kNa;
-      if (!mbar_wait_warp(&aux_full[as], (g / C::kNa) & 1, err, 331)) break;
+      const int as = g % C::kNa, buf = g % C::kBuf;
+      if (!wait_warp<kPauseSoft>(&aux_full[as], (g / C::kNa) & 1, err, 331)) break;
       const TileInfo t = *info_of(g);
       if (t.bits & kEnd) break;
       const bool keys = t.bits & kKeys;
       if (t.item != cur) {
         if (grad) flush();
         cur = t.item;
-        if (!mbar_wait_warp(&st_full[cur & 1], (cur >> 1) & 1, err, 332)) break;
+        if (!wait_warp<kPauseSoft>(&st_full[cur % C::kSlots], (cur / C::kSlots) & 1, err, 332)) break;
         const float* rv = row_vec(cur);
         add = rv[r];
         nd = keys ? 0.0f : rv[128 + r];
@@ -1055,23 +1090,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         row0 = ri * 128 + (warp & 3) * 32;
         part = ((size_t)bh * a.ditems + ri * 8 + warp) * a.buckets;
       }
-      if (!mbar_wait_warp(&s_full[wg], (g >> 1) & 1, err, 333)) break;
+      if (!wait_warp<kPauseSoft>(&s_full[buf], (g / C::kBuf) & 1, err, 333)) break;
       if (t.tile >= 0) {
         tc_fence_after();
+        const uint32_t tS = tmem + buf * 128 + lo;
         const uint8_t* ax = sAux + as * C::kAuxBytes;
-        const float* va = reinterpret_cast<const float*>(ax + C::kVecA);
-        const float* vb = reinterpret_cast<const float*>(ax + C::kVecB);
+        const float* va = reinterpret_cast<const float*>(ax + kVecs);
+        const float* vb = reinterpret_cast<const float*>(ax + kVecs + 256);
         const float row = add + t.bias;
         float far = 0.0f;
         if (keys) {
-          if (t.bits & kNear) bwd_tile<T, true, true, false>(tS, ax, C::kWin, va, vb, c2, row, nd, r, false, far, chains, lane);
-          else bwd_tile<T, true, false, false>(tS, ax, C::kWin, va, vb, c2, row, nd, r, false, far, chains, lane);
+          if (t.bits & kNear) bwd_tile<T, true, true, false>(tS, ax, kWin, va, vb, c2, row, nd, r, false, far, chains, lane);
+          else bwd_tile<T, true, false, false>(tS, ax, kWin, va, vb, c2, row, nd, r, false, far, chains, lane);
         } else if (t.bits & kNear) {
-          bwd_tile<T, false, true, true>(tS, ax, C::kWin, va, vb, c2, row, nd, r, grad, far, chains, lane);
+          bwd_tile<T, false, true, true>(tS, ax, kWin, va, vb, c2, row, nd, r, grad, far, chains, lane);
         } else if (t.bits & kMixed) {
-          bwd_tile<T, false, false, true>(tS, ax, C::kWin, va, vb, c2, row, nd, r, grad, far, chains, lane);
+          bwd_tile<T, false, false, true>(tS, ax, kWin, va, vb, c2, row, nd, r, grad, far, chains, lane);
         } else {
-          bwd_tile<T, false, false, false>(tS, ax, C::kWin, va, vb, c2, row, nd, r, grad, far, chains, lane);
+          bwd_tile<T, false, false, false>(tS, ax, kWin, va, vb, c2, row, nd, r, grad, far, chains, lane);
         }
         if (t.bits & kAhead) far_ahead += far;
         else far_behind += far;
@@ -1080,10 +1116,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&p_full[wg]);
+        mbar_arrive(&p_full[buf]);
         mbar_arrive(&aux_empty[as]);
       }
-      if (grad && (t.bits & kNear)) bin_diagonals(chains, C::kChain, a.bid + a.vec_off + t.tile * 64 - row0, bins, lane);
+      if (grad && (t.bits & kNear)) bin_diagonals(chains, kChain, a.bid + a.vec_off + t.tile * 64 - row0, bins, lane);
     }
     if (grad) flush();
   }
@@ -1138,7 +1174,7 @@ bool fwd(const AttnOp& a, cudaStream_t s) {
   return true;
 }
 
-template <typename T, int D>
+template <typename T, int D, bool LONG>
 bool bwd(const AttnOp& a, cudaStream_t s) {
   const bool bf = std::is_same<T, bf16_t>::value;
   CUtensorMap mq, mk, mv, mdo, mdq, mdk, mdv;
@@ -1147,9 +1183,9 @@ bool bwd(const AttnOp& a, cudaStream_t s) {
       !encode(&mdv, a.dv, a, bf, 128))
     return false;
   static std::atomic<uint64_t> ready{0};
-  allow_smem(attention_bwd_kernel<T, D>, Bwd<D>::kSmem, ready);
+  allow_smem(attention_bwd_kernel<T, D, LONG>, Bwd<D, LONG>::kSmem, ready);
   const int items = a.B * a.nh * ((a.S + 127) / 128);
-  launch_pdl(attention_bwd_kernel<T, D>, std::min(2 * items, sm_count()), kBwdThreads, Bwd<D>::kSmem, s, mq, mk, mv, mdo,
+  launch_pdl(attention_bwd_kernel<T, D, LONG>, std::min(2 * items, sm_count()), kBwdThreads, Bwd<D, LONG>::kSmem, s, mq, mk, mv, mdo,
              mdq, mdk, mdv, a);
   count_launch();
   return true;
@@ -1163,8 +1199,10 @@ bool attention_tc_fwd_run(int dt, const AttnOp& a, cudaStream_t s) {
 }
 
 bool attention_tc_bwd_run(int dt, const AttnOp& a, cudaStream_t s) {
-  if (dt == DT_F16) return a.d <= 64 ? bwd<half_t, 64>(a, s) : bwd<half_t, 128>(a, s);
-  return a.d <= 64 ? bwd<bf16_t, 64>(a, s) : bwd<bf16_t, 128>(a, s);
+  const bool h = dt == DT_F16;
+  if (a.d <= 64) return h ? bwd<half_t, 64, false>(a, s) : bwd<bf16_t, 64, false>(a, s);
+  if (a.S > kLongSeq) return h ? bwd<half_t, 128, true>(a, s) : bwd<bf16_t, 128, true>(a, s);
+  return h ? bwd<half_t, 128, false>(a, s) : bwd<bf16_t, 128, false>(a, s);
 }
 
 int attention_tc_take_error() {
