@@ -65,9 +65,9 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(const __grid_co
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       float* base = a.vec + ((size_t)h * 8 + s) * a.vec_len;
-      if (X - s >= 0) base[X - s] = v;
-      // direction 1: diagonal -x, at index -x + vec_off
-      const int Y = 2 * a.vec_off - X - s;
+      if (X - s - 1 >= 0) base[X - s - 1] = v;
+      // direction 1: diagonal -x
+      const int Y = 2 * a.vec_off - X - s - 1;
       if (Y >= 0 && Y < a.vec_len) base[(size_t)4 * a.vec_len + Y] = v;
     }
     return;

@@ -65,7 +65,7 @@ struct AttnOp {
 
 // The bias of diagonal x = j - i (direction 0) or x = i - j (direction 1), in
 // log2 units: copy s of a direction holds the diagonal x at index
-// x + vec_off - s, so a run that starts at any x begins 16-byte aligned in
+// x + vec_off - s - 1, so a run that starts at any x begins 16-byte aligned in
 // one of the four copies.
 __device__ __forceinline__ const float* bias_copy(const AttnOp& a, int h, int dir, int s) {
   return a.vec + ((size_t)(h * 2 + dir) * 4 + s) * a.vec_len;

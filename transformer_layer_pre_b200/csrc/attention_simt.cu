@@ -103,7 +103,7 @@ __device__ __forceinline__ void store_rows(const AttnView& v, int b, int h, int 
 // The bias of diagonal x (key minus query), log2 units.
 __device__ __forceinline__ float bias_at(const AttnOp& a, const float* vec, int x) {
   x = max(-a.sat, min(a.sat, x));
-  return vec[x + a.vec_off];
+  return vec[x + a.vec_off - 1];
 }
 
 template <int D>

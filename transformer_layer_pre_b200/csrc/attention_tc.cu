@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
       const int bh = it / nq, i = it - bh * nq, b = bh / a.nh, h = bh - b * a.nh;
       const int mb = a.mask_seqs == 1 ? 0 : b;
       const float* vec = a.vec ? bias_copy(a, h, 0, 0) : nullptr;
-      const float behind = vec ? vec[a.vec_off - a.sat] : 0.0f, ahead = vec ? vec[a.vec_off + a.sat] : 0.0f;
+      const float behind = vec ? vec[a.vec_off - a.sat - 1] : 0.0f, ahead = vec ? vec[a.vec_off + a.sat - 1] : 0.0f;
       if (lane == 0) {
         ok = wait_bar<0>(q_empty, (n & 1) ^ 1, err, 201);
         if (ok) {
@@ -432,10 +432,11 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
       bool last = false;
       for (; !last; ++g) {
         const int as = g % C::kAux;
-        if (!(ok = wait_warp<0>(&aux_full[as], (g / C::kAux) & 1, err, 221))) break;
+        // S is there, and with it the description and the vectors, which its
+        // issuing thread waited for
+        if (!(ok = wait_warp<0>(s_full, g & 1, err, 222))) break;
         const TileInfo t = *info_of(g);
         last = t.bits & kLast;
-        if (!(ok = wait_warp<0>(s_full, g & 1, err, 222))) break;
         if (t.tile < 0) {
           __syncwarp();
           if (lane == 0) {
@@ -451,8 +452,9 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
         float mul = c2, add = t.bias, m0 = -INFINITY, m1 = -INFINITY;
         const uint8_t* ax = sAux + as * C::kAuxBytes;
         if (t.bits & (kNear | kMixed)) {
-          // row r's run of diagonals starts at 128 - r of the window
-          const int start = 128 - r;
+          // row r's run of diagonals starts at 128 - r of the window (copy s is
+          // shifted by s + 1)
+          const int start = 127 - r;
           const float* wnd = reinterpret_cast<const float*>(ax) + (start & 3) * C::kWin + (start & ~3);
           const float* mrow = reinterpret_cast<const float*>(ax + 4 * C::kWin * 4);
           const bool near = t.bits & kNear, mixed = t.bits & kMixed;
@@ -622,10 +624,9 @@ struct Bwd {
   static constexpr int kBuf = 2;                                    // S, dP buffers
   static constexpr int kAcc = D == 64 ? 2 : 1;                      // sets of sums
   static constexpr uint32_t kSums = kBuf * 128;                     // their first TMEM column
-  static constexpr int kNa = D == 64 ? 6 : 4;                       // tile descriptions
-  static constexpr int kAuxBytes = kVecs + 512 + 16;
+  static constexpr int kAuxBytes = kVecs + 512 + 16;                // window, two column vectors, description
   static constexpr int kStAux = 2 * 128 * 4 + 16;                   // row vectors, empty flag
-  static constexpr int kSmem = kSlots * 2 * kSt + 2 * kNs * kMv + kNa * kAuxBytes + kSlots * kStAux +
+  static constexpr int kSmem = kSlots * 2 * kSt + 2 * kNs * kMv + kNs * kAuxBytes + kSlots * kStAux +
                                8 * kAttnMaxBuckets * 4 + 8 * 4 * kChain * 4 + 400;
   static_assert(kSums + kAcc * 2 * D <= 512, "the sums do not fit the tensor memory");
   static_assert(kSmem <= 227 * 1024, "the backward's shared memory exceeds a block's maximum");
@@ -694,7 +695,7 @@ template <typename T, bool KEYS, bool NEAR, bool MIX>
 __device__ __forceinline__ void bwd_tile(uint32_t tS, const uint8_t* ax, int win, const float* vecA, const float* vecB,
                                          float c2, float row, float nd_row, int r, bool grad, float& far_sum,
                                          float* chains, int lane) {
-  const int start = 128 - r;
+  const int start = 127 - r;   // the row's run of diagonals; copy s is shifted by s + 1
   const float* wnd = reinterpret_cast<const float*>(ax) + (start & 3) * win + (start & ~3);
   float2 fs = f2(0.0f);
 #pragma unroll
@@ -756,6 +757,8 @@ template <typename T, int D, bool LONG>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     attention_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                          const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
+                         const __grid_constant__ CUtensorMap tq2, const __grid_constant__ CUtensorMap tk2,
+                         const __grid_constant__ CUtensorMap tv2, const __grid_constant__ CUtensorMap tdo2,
                          const __grid_constant__ CUtensorMap tdq, const __grid_constant__ CUtensorMap tdk,
                          const __grid_constant__ CUtensorMap tdv, const __grid_constant__ AttnOp a) {
   using C = Bwd<D, LONG>;
@@ -763,14 +766,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sSt = smem_raw;                                  // [kSlots] x (A1, A2)
   uint8_t* sMv = sSt + C::kSlots * 2 * C::kSt;                          // [kNs] x (B1, B2)
-  uint8_t* sAux = sMv + 2 * C::kNs * C::kMv;                // [kNa]
-  uint8_t* sStAux = sAux + C::kNa * C::kAuxBytes;           // [2]
+  uint8_t* sAux = sMv + 2 * C::kNs * C::kMv;                // [kNs]
+  uint8_t* sStAux = sAux + C::kNs * C::kAuxBytes;           // [2]
   float* sBins = reinterpret_cast<float*>(sStAux + C::kSlots * C::kStAux);
   float* sChains = sBins + 8 * kAttnMaxBuckets;
   uint64_t* bar = reinterpret_cast<uint64_t*>(sChains + 8 * 4 * kChain);
   uint64_t *st_full = bar, *st_empty = st_full + C::kSlots, *mv_full = st_empty + C::kSlots,
-           *mv_empty = mv_full + C::kNs, *aux_full = mv_empty + C::kNs, *aux_empty = aux_full + C::kNa,
-           *s_full = aux_empty + C::kNa, *p_full = s_full + C::kBuf, *s_free = p_full + C::kBuf,
+           *mv_empty = mv_full + C::kNs, *s_full = mv_empty + C::kNs, *p_full = s_full + C::kBuf, *s_free = p_full + C::kBuf,
            *acc_full = s_free + C::kBuf, *acc_free = acc_full + C::kAcc;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(acc_free + C::kAcc);
 
@@ -780,7 +782,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     for (int i = 0; i < C::kSlots; ++i) mbar_init(&st_full[i], 1), mbar_init(&st_empty[i], 1);
     for (int i = 0; i < C::kBuf; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 4), mbar_init(&s_free[i], 1);
     for (int i = 0; i < C::kNs; ++i) mbar_init(&mv_full[i], 1), mbar_init(&mv_empty[i], 1);
-    for (int i = 0; i < C::kNa; ++i) mbar_init(&aux_full[i], 1), mbar_init(&aux_empty[i], 6);
     for (int i = 0; i < C::kAcc; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_free[i], 4);
     fence_barrier_init();
   }
@@ -795,15 +796,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int nr = (a.S + 127) / 128, nm = (a.S + 63) / 64;
   const int items = a.B * a.nh * nr;
   auto info_of = [&](uint32_t g) -> TileInfo* {
-    return reinterpret_cast<TileInfo*>(sAux + (g % C::kNa) * C::kAuxBytes + kVecs + 512);
+    return reinterpret_cast<TileInfo*>(sAux + (g % C::kNs) * C::kAuxBytes + kVecs + 512);
   };
   auto row_vec = [&](int n) { return reinterpret_cast<float*>(sStAux + (n % C::kSlots) * C::kStAux); };
   auto none_flag = [&](int n) { return reinterpret_cast<int*>(sStAux + (n % C::kSlots) * C::kStAux + 1024); };
 
   if (warp == 12) {
     // ---- producer
-    uint32_t g = 0, mc = 0;
-    uint32_t st_issued = 0, mv_issued = 0, aux_issued = 0;
+    uint32_t g = 0, st_issued = 0;
     int n = 0;
     bool ok = true;
     for (int it = blockIdx.x; it < 2 * items && ok; it += gridDim.x, ++n) {
@@ -812,7 +812,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const int mb = a.mask_seqs == 1 ? 0 : b;
       const int* flags = a.flags + mb * (a.Sp / kAttnFlagKeys);
       const float* vec = a.vec ? bias_copy(a, h, 0, 0) : nullptr;
-      const float behind = vec ? vec[a.vec_off - a.sat] : 0.0f, ahead = vec ? vec[a.vec_off + a.sat] : 0.0f;
+      const float behind = vec ? vec[a.vec_off - a.sat - 1] : 0.0f, ahead = vec ? vec[a.vec_off + a.sat - 1] : 0.0f;
+      const float* stats = a.stats + (size_t)bh * 2 * a.Sp;
+      const float* col = keys ? stats + (lane == 9 ? a.Sp : 0) : a.maskx + (size_t)mb * a.Sp;
       LiveTiles<1> tiles(flags, nm, lane);
       bool mix = false;
       int j = keys ? (flags[2 * ri] == 2 && flags[2 * ri + 1] == 2 ? nm : 0) : tiles.next(0, mix);
@@ -823,12 +825,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         ++st_issued;
         mbar_arrive_expect_tx(&st_full[slot], 2 * C::kSt + (keys ? 512 : 1024));
         uint8_t* st = sSt + slot * 2 * C::kSt;
-        for (int c = 0; c < D / 64; ++c)
-          for (int t = 0; t < 2; ++t) {
-            tma_load_4d(st + c * kRegion + t * 8192, keys ? &tk : &tq, &st_full[slot], c * 64, ri * 128 + t * 64, h, b);
-            tma_load_4d(st + C::kSt + c * kRegion + t * 8192, keys ? &tv : &tdo, &st_full[slot], c * 64,
-                        ri * 128 + t * 64, h, b);
-          }
+        for (int c = 0; c < D / 64; ++c) {
+          tma_load_4d(st + c * kRegion, keys ? &tk2 : &tq2, &st_full[slot], c * 64, ri * 128, h, b);
+          tma_load_4d(st + C::kSt + c * kRegion, keys ? &tv2 : &tdo2, &st_full[slot], c * 64, ri * 128, h, b);
+        }
         if (keys) {
           bulk_load_1d(row_vec(n), a.maskx + (size_t)mb * a.Sp + ri * 128, 512, &st_full[slot]);
         } else {
@@ -841,99 +841,82 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       do {
         bool nmix = false;
         const int jn = none ? nm : (keys ? j + 1 : tiles.next(j + 1, nmix));
-        if (lane == 0 && ok) {
-          const int as = g % C::kNa;
-          TileInfo t;
-          t.tile = none ? -1 : j;
-          t.item = n;
-          t.bits = (jn == nm ? kLast : 0) | (first ? kFirst : 0) | (keys ? kKeys : 0);
-          t.bias = 0.0f;
-          // diagonal of the tile's corner, column minus row
-          const int x0 = j * 64 - ri * 128;
-          if (!none) {
-            if (vec) {
-              // key minus query: the columns are the keys, or the rows are
-              const int lo = keys ? -(x0 + 63) : x0 - 127, hi = keys ? 127 - x0 : x0 + 63;
-              if (lo >= a.sat) t.bias = ahead, t.bits |= kAhead;
-              else if (hi <= -a.sat) t.bias = behind;
-              else t.bits |= kNear;
-            }
-            if (mix && !keys) t.bits |= kMixed;
+        const int ms = g % C::kNs;
+        TileInfo t;
+        t.tile = none ? -1 : j;
+        t.item = n;
+        t.bits = (jn == nm ? kLast : 0) | (first ? kFirst : 0) | (keys ? kKeys : 0);
+        t.bias = 0.0f;
+        // diagonal of the tile's corner, column minus row
+        const int x0 = j * 64 - ri * 128;
+        if (!none) {
+          if (vec) {
+            // key minus query: the columns are the keys, or the rows are
+            const int lo = keys ? -(x0 + 63) : x0 - 127, hi = keys ? 127 - x0 : x0 + 63;
+            if (lo >= a.sat) t.bias = ahead, t.bits |= kAhead;
+            else if (hi <= -a.sat) t.bias = behind;
+            else t.bits |= kNear;
           }
-          if ((ok = wait_bar<kPauseLoad>(&aux_empty[as], ((g / C::kNa) & 1) ^ 1, err, 302))) {
-            uint8_t* ax = sAux + as * C::kAuxBytes;
-            *info_of(g) = t;
-            const bool near = t.bits & kNear, va = !none && (keys || near || (t.bits & kMixed));
-            ++aux_issued;
-            mbar_arrive_expect_tx(&aux_full[as], (near ? 4 * kRun * 4 : 0) + (va ? 256 : 0) + (keys && !none ? 256 : 0));
-            if (near)
-              for (int s = 0; s < 4; ++s)
-                bulk_load_1d(ax + s * kWin * 4, bias_copy(a, h, keys ? 1 : 0, s) + x0 - 128 + a.vec_off, kRun * 4,
-                             &aux_full[as]);
-            if (va)
-              bulk_load_1d(ax + kVecs,
-                           (keys ? a.stats + (size_t)bh * 2 * a.Sp : a.maskx + (size_t)mb * a.Sp) + j * 64, 256,
-                           &aux_full[as]);
-            if (keys && !none)
-              bulk_load_1d(ax + kVecs + 256, a.stats + (size_t)bh * 2 * a.Sp + a.Sp + j * 64, 256, &aux_full[as]);
-          }
-          if (ok && !none) {
-            const int ms = mc % C::kNs;
-            if ((ok = wait_bar<kPauseLoad>(&mv_empty[ms], ((mc / C::kNs) & 1) ^ 1, err, 303))) {
-              ++mv_issued;
-              mbar_arrive_expect_tx(&mv_full[ms], 2 * C::kMv);
-              uint8_t* mv = sMv + ms * 2 * C::kMv;
-              for (int c = 0; c < D / 64; ++c) {
-                tma_load_4d(mv + c * C::kMvRegion, keys ? &tq : &tk, &mv_full[ms], c * 64, j * 64, h, b);
-                tma_load_4d(mv + C::kMv + c * C::kMvRegion, keys ? &tdo : &tv, &mv_full[ms], c * 64, j * 64, h, b);
-              }
-            }
-          }
+          if (mix && !keys) t.bits |= kMixed;
+        }
+        const bool near = t.bits & kNear, one = !none && (keys || near || (t.bits & kMixed)), two = !none && keys;
+        if (lane == 0 && ok && (ok = wait_bar<kPauseLoad>(&mv_empty[ms], ((g / C::kNs) & 1) ^ 1, err, 303))) {
+          *info_of(g) = t;
+          mbar_arrive_expect_tx(&mv_full[ms], (near ? 4 * kRun * 4 : 0) + (one ? 256 : 0) + (two ? 256 : 0) +
+                                                  (none ? 0 : 2 * C::kMv));
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        // a lane per copy
+        uint8_t* ax = sAux + ms * C::kAuxBytes;
+        uint8_t* mv = sMv + ms * 2 * C::kMv;
+        if (lane < 2 * D / 64) {
+          const int c = lane >> 1;
+          if (!none)
+            tma_load_4d(mv + (lane & 1) * C::kMv + c * C::kMvRegion,
+                        lane & 1 ? (keys ? &tdo : &tv) : (keys ? &tq : &tk), &mv_full[ms], c * 64, j * 64, h, b);
+        } else if (lane >= 4 && lane < 8) {
+          if (near)
+            bulk_load_1d(ax + (lane - 4) * kWin * 4, bias_copy(a, h, keys ? 1 : 0, lane - 4) + x0 - 128 + a.vec_off,
+                         kRun * 4, &mv_full[ms]);
+        } else if (lane == 8 || lane == 9) {
+          if (lane == 8 ? one : two) bulk_load_1d(ax + kVecs + (lane - 8) * 256, col + j * 64, 256, &mv_full[ms]);
+        }
+        __syncwarp();
         first = false;
         ++g;
-        if (!none) ++mc;
         j = jn;
         mix = nmix;
-      } while (ok && j < nm);
+      } while (j < nm);
     }
-    // the end, for either softmax group (the issuing threads stop at the first)
+    // the end, for either softmax group
     for (int e = 0; e < 2 && ok && lane == 0; ++e, ++g) {
-      if (!(ok = wait_bar<kPauseLoad>(&aux_empty[g % C::kNa], ((g / C::kNa) & 1) ^ 1, err, 304))) break;
-      TileInfo t = {-1, kEnd, 0.0f, -1};
-      *info_of(g) = t;
-      ++aux_issued;
-      mbar_arrive(&aux_full[g % C::kNa]);
+      if (!(ok = wait_bar<kPauseLoad>(&mv_empty[g % C::kNs], ((g / C::kNs) & 1) ^ 1, err, 304))) break;
+      *info_of(g) = TileInfo{-1, kEnd, 0.0f, -1};
+      mbar_arrive(&mv_full[g % C::kNs]);
     }
     if (!ok && lane == 0) {
       drain<C::kSlots>(st_full, st_issued);
-      drain<C::kNs>(mv_full, mv_issued);
-      drain<C::kNa>(aux_full, aux_issued);
+      drain<C::kNs>(mv_full, g);
     }
   } else if (warp == 13) {
     // ---- S and dP of each tile, as soon as its operands and a buffer are there
     if (lane == 0) {
       const uint32_t id = idesc_f16(128, 64, std::is_same<T, bf16_t>::value, false, false);
       const uint64_t dst = desc_k(smem_u32(sSt), 0, kRegion), dmv = desc_k(smem_u32(sMv), 0, C::kMvRegion);
-      uint32_t mc = 0;
-      for (uint32_t g = 0;; ++g) {
-        const int as = g % C::kNa, w = g % C::kBuf;
-        if (!wait_bar<0>(&aux_full[as], (g / C::kNa) & 1, err, 313)) break;
+      for (uint32_t g = 0, ends = 0; ends < 2; ++g) {
+        const int ms = g % C::kNs, w = g % C::kBuf;
+        if (!wait_bar<0>(&mv_full[ms], (g / C::kNs) & 1, err, 313)) break;
         const TileInfo t = *info_of(g);
-        mbar_arrive(&aux_empty[as]);
-        if (t.bits & kEnd) break;
         const int slot = t.item % C::kSlots;
         if ((t.bits & kFirst) && !wait_bar<0>(&st_full[slot], (t.item / C::kSlots) & 1, err, 314)) break;
         // the buffer's last tile has been multiplied out of it
         if (!wait_bar<0>(&s_free[w], ((g / C::kBuf) & 1) ^ 1, err, 316)) break;
         if (t.tile < 0) {
+          if (t.bits & kEnd) ++ends;
           mbar_arrive(&s_full[w]);
           continue;
         }
-        const int ms = mc % C::kNs;
-        if (!wait_bar<0>(&mv_full[ms], (mc / C::kNs) & 1, err, 315)) break;
-        ++mc;
         tc_fence_after();
         const uint64_t a1 = dst + slot * (2 * C::kSt >> 4), a2 = a1 + (C::kSt >> 4);
         const uint64_t b1 = dmv + ms * (2 * C::kMv >> 4), b2 = b1 + (C::kMv >> 4);
@@ -954,24 +937,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (lane == 0) {
       const uint32_t id = idesc_f16(128, D, std::is_same<T, bf16_t>::value, false, true);
       const uint64_t dmn = desc_mn(smem_u32(sMv), 0, C::kMvRegion);
-      uint32_t mc = 0;
-      for (uint32_t g = 0;; ++g) {
-        const int as = g % C::kNa, w = g % C::kBuf;
-        if (!wait_bar<0>(&aux_full[as], (g / C::kNa) & 1, err, 317)) break;
+      for (uint32_t g = 0, ends = 0; ends < 2; ++g) {
+        const int ms = g % C::kNs, w = g % C::kBuf;
+        if (!wait_bar<0>(&p_full[w], (g / C::kBuf) & 1, err, 311)) break;
         const TileInfo t = *info_of(g);
-        mbar_arrive(&aux_empty[as]);
-        if (t.bits & kEnd) break;
         const int ab = t.item % C::kAcc;
         if ((t.bits & kFirst) && !wait_bar<0>(&acc_free[ab], ((t.item / C::kAcc) & 1) ^ 1, err, 312)) break;
-        if (!wait_bar<0>(&p_full[w], (g / C::kBuf) & 1, err, 311)) break;
         if (t.tile < 0) {
+          mbar_arrive(&mv_empty[ms]);
           mbar_arrive(&s_free[w]);
-          mbar_arrive(&acc_full[ab]);
+          if (t.bits & kEnd) ++ends;
+          else mbar_arrive(&acc_full[ab]);
           continue;
         }
         tc_fence_after();
-        const int ms = mc % C::kNs;
-        ++mc;
         const uint32_t acc1 = tmem + C::kSums + ab * 2 * D, acc2 = acc1 + D, tS = tmem + w * 128;
         const uint64_t b1 = dmn + ms * (2 * C::kMv >> 4), b2 = b1 + (C::kMv >> 4);
         const uint32_t more = t.bits & kFirst ? 0u : 1u;
@@ -1054,33 +1033,41 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     __syncwarp();
     int cur = -1, row0 = 0;
     size_t part = 0;               // this warp's row of dpart for the current item
-    bool grad = false;
+    bool grad = false, any_far = false;
     float add = 0.0f, nd = 0.0f, far_behind = 0.0f, far_ahead = 0.0f;
     // the item's bias gradient: this warp's share
     auto flush = [&]() {
-      const float fb = warp_sum(far_behind), fa = warp_sum(far_ahead);
-      if (lane == 0) {
-        bins[a.buckets / 2 - 1] += fb;
-        bins[a.buckets - 1] += fa;
+      if (any_far) {
+        const float fb = warp_sum(far_behind), fa = warp_sum(far_ahead);
+        if (lane == 0) {
+          bins[a.buckets / 2 - 1] += fb;
+          bins[a.buckets - 1] += fa;
+        }
+        __syncwarp();
+        far_behind = far_ahead = 0.0f;
+        any_far = false;
       }
-      __syncwarp();
       for (int u = lane; u < a.buckets; u += 32) {
         a.dpart[part + u] = bins[u];
         bins[u] = 0.0f;
       }
       __syncwarp();
-      far_behind = far_ahead = 0.0f;
     };
     for (uint32_t g = wg;; g += 2) {
-      const int as = g % C::kNa, buf = g % C::kBuf;
-      if (!wait_warp<kPauseSoft>(&aux_full[as], (g / C::kNa) & 1, err, 331)) break;
+      const int buf = g % C::kBuf;
+      // S is there, and with it everything that its issuing thread waited for:
+      // the description, the vectors, the item's row vectors (each wait costs
+      // 150 clocks even when there is nothing to wait for)
+      if (!wait_warp<kPauseSoft>(&s_full[buf], (g / C::kBuf) & 1, err, 333)) break;
       const TileInfo t = *info_of(g);
-      if (t.bits & kEnd) break;
+      if (t.bits & kEnd) {
+        if (lane == 0) mbar_arrive(&p_full[buf]);
+        break;
+      }
       const bool keys = t.bits & kKeys;
       if (t.item != cur) {
         if (grad) flush();
         cur = t.item;
-        if (!wait_warp<kPauseSoft>(&st_full[cur % C::kSlots], (cur / C::kSlots) & 1, err, 332)) break;
         const float* rv = row_vec(cur);
         add = rv[r];
         nd = keys ? 0.0f : rv[128 + r];
@@ -1090,11 +1077,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         row0 = ri * 128 + (warp & 3) * 32;
         part = ((size_t)bh * a.ditems + ri * 8 + warp) * a.buckets;
       }
-      if (!wait_warp<kPauseSoft>(&s_full[buf], (g / C::kBuf) & 1, err, 333)) break;
       if (t.tile >= 0) {
         tc_fence_after();
         const uint32_t tS = tmem + buf * 128 + lo;
-        const uint8_t* ax = sAux + as * C::kAuxBytes;
+        const uint8_t* ax = sAux + (g % C::kNs) * C::kAuxBytes;
         const float* va = reinterpret_cast<const float*>(ax + kVecs);
         const float* vb = reinterpret_cast<const float*>(ax + kVecs + 256);
         const float row = add + t.bias;
@@ -1109,16 +1095,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         } else {
           bwd_tile<T, false, false, false>(tS, ax, kWin, va, vb, c2, row, nd, r, grad, far, chains, lane);
         }
-        if (t.bits & kAhead) far_ahead += far;
-        else far_behind += far;
+        if (!(t.bits & kNear)) {
+          any_far = true;
+          if (t.bits & kAhead) far_ahead += far;
+          else far_behind += far;
+        }
         tmem_store_wait();
         tc_fence_before();
       }
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&p_full[buf]);
-        mbar_arrive(&aux_empty[as]);
-      }
+      if (lane == 0) mbar_arrive(&p_full[buf]);
       if (grad && (t.bits & kNear)) bin_diagonals(chains, kChain, a.bid + a.vec_off + t.tile * 64 - row0, bins, lane);
     }
     if (grad) flush();
@@ -1177,16 +1163,17 @@ bool fwd(const AttnOp& a, cudaStream_t s) {
 template <typename T, int D, bool LONG>
 bool bwd(const AttnOp& a, cudaStream_t s) {
   const bool bf = std::is_same<T, bf16_t>::value;
-  CUtensorMap mq, mk, mv, mdo, mdq, mdk, mdv;
+  CUtensorMap mq, mk, mv, mdo, mq2, mk2, mv2, mdo2, mdq, mdk, mdv;   // in boxes of 64 and of 128 tokens
   if (!encode(&mq, a.q, a, bf, 64) || !encode(&mk, a.k, a, bf, 64) || !encode(&mv, a.v, a, bf, 64) ||
-      !encode(&mdo, a.dout, a, bf, 64) || !encode(&mdq, a.dq, a, bf, 128) || !encode(&mdk, a.dk, a, bf, 128) ||
+      !encode(&mdo, a.dout, a, bf, 64) || !encode(&mq2, a.q, a, bf, 128) || !encode(&mk2, a.k, a, bf, 128) ||
+      !encode(&mv2, a.v, a, bf, 128) || !encode(&mdo2, a.dout, a, bf, 128) || !encode(&mdq, a.dq, a, bf, 128) || !encode(&mdk, a.dk, a, bf, 128) ||
       !encode(&mdv, a.dv, a, bf, 128))
     return false;
   static std::atomic<uint64_t> ready{0};
   allow_smem(attention_bwd_kernel<T, D, LONG>, Bwd<D, LONG>::kSmem, ready);
   const int items = a.B * a.nh * ((a.S + 127) / 128);
   launch_pdl(attention_bwd_kernel<T, D, LONG>, std::min(2 * items, sm_count()), kBwdThreads, Bwd<D, LONG>::kSmem, s, mq, mk, mv, mdo,
-             mdq, mdk, mdv, a);
+             mq2, mk2, mv2, mdo2, mdq, mdk, mdv, a);
   count_launch();
   return true;
 }
