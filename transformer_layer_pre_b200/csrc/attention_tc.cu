@@ -621,8 +621,8 @@ struct Bwd {
   static constexpr int kMv = D / 64 * kMvRegion;                    // a moving tile
   static constexpr int kSlots = D == 128 && LONG ? 1 : 2;           // stationary pairs
   static constexpr int kNs = D == 64 || LONG ? 4 : 2;               // moving pairs
-  static constexpr int kBuf = 2;                                    // S, dP buffers
-  static constexpr int kAcc = D == 64 ? 2 : 1;                      // sets of sums
+  static constexpr int kBuf = D == 64 && LONG ? 3 : 2;              // S, dP buffers
+  static constexpr int kAcc = D == 64 && !LONG ? 2 : 1;             // sets of sums
   static constexpr uint32_t kSums = kBuf * 128;                     // their first TMEM column
   static constexpr int kAuxBytes = kVecs + 512 + 16;                // window, two column vectors, description
   static constexpr int kStAux = 2 * 128 * 4 + 16;                   // row vectors, empty flag
@@ -631,9 +631,12 @@ struct Bwd {
   static_assert(kSums + kAcc * 2 * D <= 512, "the sums do not fit the tensor memory");
   static_assert(kSmem <= 227 * 1024, "the backward's shared memory exceeds a block's maximum");
 };
-// D = 128 from this length on: one stationary pair and four moving ones instead
-// of two and two (shared memory holds six).  B4 h8 S2048: 310 us against 344;
-// B8 h8 S512, whose items are short: 84 against 82.
+// LONG, from this length on: for D = 128 one stationary pair and four moving
+// ones instead of two and two (shared memory holds six), for D = 64 a third
+// buffer of S and dP instead of a second set of sums.  B4 h8 d128 S2048: 310 us
+// against 344; B4 h16 d64 S2048: 409 against 434.  Short sequences, whose items
+// are over sooner, lose by it: B8 h8 d128 S512 84 us against 82, B16 h16 d64
+// S512 170 against 167.
 constexpr int kLongSeq = 1024;
 constexpr int kBwdThreads = 480;
 constexpr int kPauseLoad = 50, kPauseSoft = 20, kPauseStore = 200;   // ns between polls
@@ -1187,8 +1190,11 @@ bool attention_tc_fwd_run(int dt, const AttnOp& a, cudaStream_t s) {
 
 bool attention_tc_bwd_run(int dt, const AttnOp& a, cudaStream_t s) {
   const bool h = dt == DT_F16;
+  if (a.S > kLongSeq) {
+    if (a.d <= 64) return h ? bwd<half_t, 64, true>(a, s) : bwd<bf16_t, 64, true>(a, s);
+    return h ? bwd<half_t, 128, true>(a, s) : bwd<bf16_t, 128, true>(a, s);
+  }
   if (a.d <= 64) return h ? bwd<half_t, 64, false>(a, s) : bwd<bf16_t, 64, false>(a, s);
-  if (a.S > kLongSeq) return h ? bwd<half_t, 128, true>(a, s) : bwd<bf16_t, 128, true>(a, s);
   return h ? bwd<half_t, 128, false>(a, s) : bwd<bf16_t, 128, false>(a, s);
 }
 
