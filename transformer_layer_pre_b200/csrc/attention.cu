@@ -15,12 +15,13 @@ namespace tlp {
 namespace {
 
 constexpr int kPrepThreads = 256;
+constexpr int kPrepRows = 4;        // rows of O and dO in flight per group of lanes
 
 // One launch fills the workspace (layout at the top of attention.cuh).
 // Blocks [0, nmask): 256 keys each of maskx and flags.  Then nvec blocks: 256
 // diagonals of one head each, written to every copy.  Then (backward) nzero
 // blocks that clear dpart, and blocks
-// of 256 / G rows for stats, G lanes per row reading 16 bytes each; rows run
+// of 4 * 256 / G rows for stats, G lanes per row reading 16 bytes each; rows run
 // (b, token, head) with the head fastest, the order in which O and dO lie in
 // (B, S, heads, d) memory.
 // Bound: HBM in the backward (reads O and dO once), launch latency otherwise.
@@ -80,16 +81,20 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(const __grid_co
   }
   blk -= nzero;
   constexpr int kEl = 16 / sizeof(T);
-  const long long row = (long long)blk * (kPrepThreads / G) + tid / G;
-  const long long rows = (long long)a.B * a.Sp * a.nh;
   const int lane = tid % G;
-  float t = 0.0f;
-  int b = 0, i = 0, h = 0;
-  if (row < rows) {
-    h = (int)(row % a.nh);
-    i = (int)(row / a.nh % a.Sp);
-    b = (int)(row / a.nh / a.Sp);
-    if (i < a.S)
+  const unsigned rows = (unsigned)a.B * a.Sp * a.nh;    // at most 2^30
+  unsigned row[kPrepRows];
+  float t[kPrepRows];
+  size_t at[kPrepRows];                                 // of the row's stats
+  int tok[kPrepRows];
+#pragma unroll
+  for (int k = 0; k < kPrepRows; ++k) {
+    row[k] = ((unsigned)blk * kPrepRows + k) * (kPrepThreads / G) + tid / G;
+    const unsigned r = min(row[k], rows - 1), bt = r / a.nh, h = r - bt * a.nh, b = bt / a.Sp, i = bt - b * a.Sp;
+    tok[k] = i;
+    at[k] = (size_t)b * a.nh + h;
+    t[k] = 0.0f;
+    if ((int)i < a.S)
       for (int c = lane * kEl; c < a.d; c += G * kEl) {
         const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.o.p) + (size_t)b * a.o.sb +
                                                         (size_t)i * a.o.st + (size_t)h * a.o.sh + c);
@@ -97,41 +102,45 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(const __grid_co
                                                         (size_t)i * a.dout.st + (size_t)h * a.dout.sh + c);
         const T *xe = reinterpret_cast<const T*>(&x), *ye = reinterpret_cast<const T*>(&y);
 #pragma unroll
-        for (int k = 0; k < kEl; ++k) t = fmaf(to_f(xe[k]), to_f(ye[k]), t);
+        for (int e = 0; e < kEl; ++e) t[k] = fmaf(to_f(xe[e]), to_f(ye[e]), t[k]);
       }
   }
 #pragma unroll
-  for (int w = G / 2; w > 0; w >>= 1) t += __shfl_xor_sync(0xffffffffu, t, w);
-  if (row < rows && lane == 0) {
-    const size_t bh = (size_t)b * a.nh + h;
-    float* st = a.stats + bh * 2 * a.Sp;
-    st[i] = i < a.S ? -a.lse[bh * a.S + i] * kAttnLog2e : -INFINITY;
-    st[a.Sp + i] = i < a.S ? -t : 0.0f;
+  for (int k = 0; k < kPrepRows; ++k) {
+#pragma unroll
+    for (int w = G / 2; w > 0; w >>= 1) t[k] += __shfl_xor_sync(0xffffffffu, t[k], w);
+    if (row[k] < rows && lane == 0) {
+      const int i = tok[k];
+      float* st = a.stats + at[k] * 2 * a.Sp;
+      st[i] = i < a.S ? -a.lse[at[k] * a.S + i] * kAttnLog2e : -INFINITY;
+      st[a.Sp + i] = i < a.S ? -t[k] : 0.0f;
+    }
   }
 }
 
 // dtable[u, h] (+)= sum over sequences and items of dpart, in a fixed order
 // and in float64: a block per head and 32 buckets, a lane per bucket (whole
 // lines of dpart), the rows dealt to the warps.
-constexpr int kTableWarps = 16;
+constexpr int kTableWarps = 32;
 __global__ void __launch_bounds__(32 * kTableWarps) attn_table_grad_kernel(const __grid_constant__ AttnOp a) {
   __shared__ double red[kTableWarps][33];
   pdl_wait();
   pdl_launch_dependents();
   const int h = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, u = blockIdx.y * 32 + lane;
-  const long long rows = (long long)a.B * a.ditems;
+  const unsigned rows = (unsigned)a.B * a.ditems, per = a.ditems;   // below 2^30
   double t = 0.0;
   if (u < a.buckets) {
-#pragma unroll 4
-    for (long long r = warp; r < rows; r += kTableWarps) {
-      const long long b = r / a.ditems, it = r - b * a.ditems;
-      t += (double)a.dpart[((b * a.nh + h) * a.ditems + it) * a.buckets + u];
+#pragma unroll 8
+    for (unsigned r = warp; r < rows; r += kTableWarps) {
+      const unsigned b = r / per;
+      t += (double)a.dpart[((size_t)(b * a.nh + h) * per + (r - b * per)) * a.buckets + u];
     }
   }
   red[warp][lane] = t;
   __syncthreads();
   if (warp == 0 && u < a.buckets) {
     t = 0.0;
+#pragma unroll
     for (int w = 0; w < kTableWarps; ++w) t += red[w][lane];
     float* d = a.dtable + (size_t)u * a.nh + h;
     *d = (float)(a.daccumulate ? (double)*d + t : t);
@@ -144,7 +153,8 @@ void prep(const AttnOp& a, bool backward, cudaStream_t s) {
   const int nvec = a.vec ? a.nh * ((a.vec_len + kPrepThreads - 1) / kPrepThreads) : 0;
   const int nzero = a.dpart ? 64 : 0;
   const long long rows = backward ? (long long)a.B * a.Sp * a.nh : 0;
-  const int nrow = (int)((rows + kPrepThreads / G - 1) / (kPrepThreads / G));
+  constexpr int per = kPrepRows * (kPrepThreads / G);
+  const int nrow = (int)((rows + per - 1) / per);
   launch_pdl(attn_prep_kernel<T, G>, nmask + nvec + nzero + nrow, kPrepThreads, 0, s, a, nmask, nvec, nzero);
   count_launch();
 }
