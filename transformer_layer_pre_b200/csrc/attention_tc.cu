@@ -613,7 +613,8 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
 // sets of them for D = 64, so the next item starts while one is written out.
 constexpr int kRun = 192, kWin = 200;           // diagonals of a 128 x 64 tile, floats of a window copy
 constexpr int kVecs = 4 * kWin * 4;             // column vectors after the four copies
-constexpr int kChain = 48;                      // floats of a diagonal chain
+constexpr int kChain = 40;                      // floats of a diagonal chain
+constexpr int kChains = 8;                      // of a tile's 64 columns, 8 each
 template <int D, bool LONG>
 struct Bwd {
   static constexpr int kSt = D / 64 * kRegion;                      // a stationary tile
@@ -627,7 +628,7 @@ struct Bwd {
   static constexpr int kAuxBytes = kVecs + 512 + 16;                // window, two column vectors, description
   static constexpr int kStAux = 2 * 128 * 4 + 16;                   // row vectors, empty flag
   static constexpr int kSmem = kSlots * 2 * kSt + 2 * kNs * kMv + kNs * kAuxBytes + kSlots * kStAux +
-                               8 * kAttnMaxBuckets * 4 + 8 * 4 * kChain * 4 + 400;
+                               8 * kAttnMaxBuckets * 4 + 8 * kChains * kChain * 4 + 400;
   static_assert(kSums + kAcc * 2 * D <= 512, "the sums do not fit the tensor memory");
   static_assert(kSmem <= 227 * 1024, "the backward's shared memory exceeds a block's maximum");
 };
@@ -641,52 +642,61 @@ constexpr int kLongSeq = 1024;
 constexpr int kBwdThreads = 480;
 constexpr int kPauseLoad = 50, kPauseSoft = 20, kPauseStore = 200;   // ns between polls
 
-// Sums the diagonals of a warp's 32 rows x 16 columns (v: this lane's row).
-// Diagonal t - lane moves up one lane per column, so the running sums are
-// shifted along; the one that leaves at lane 31 is done and goes to
-// out[t], the 32 left at the end to out[16 ..], in order of the diagonal:
-// out[y] is diagonal y - 31.
-__device__ __forceinline__ void diagonal_chain(const float* v, float* out, int lane) {
-  float s = 0.0f;
+// Sums the diagonals of a warp's 32 rows x 32 columns (v: this lane's row), as
+// four chains of 8 columns whose steps are independent of one another.  Diagonal
+// t - lane moves up one lane per column, so a chain's running sums are shifted
+// along; the one that leaves at lane 31 is done and goes to out[t], the 32 left
+// at the end to out[8 ..], in order of the diagonal: out[y] is diagonal y - 31.
+__device__ __forceinline__ void diagonal_chains(const float (&v)[32], float* out, int lane) {
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int t = 0; t < 16; ++t) {
-    s += v[t];
-    if (t < 15) {
-      if (lane == 31) out[t] = s;
-      s = __shfl_up_sync(0xffffffffu, s, 1);
-      if (lane == 0) s = 0.0f;
+  for (int t = 0; t < 8; ++t) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) s[c] += v[8 * c + t];
+    if (t < 7) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (lane == 31) out[c * kChain + t] = s[c];
+        s[c] = __shfl_up_sync(0xffffffffu, s[c], 1);
+        if (lane == 0) s[c] = 0.0f;
+      }
     }
   }
-  out[46 - lane] = s;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) out[c * kChain + 38 - lane] = s[c];
 }
 
-// One warp's 32 rows x 64 columns of dS, from its four chains into its bins:
-// each of the 95 diagonals is the sum of the chains that cross it; those of one
-// bucket are neighbours and are summed by a segmented scan.  bid: the bucket of
-// diagonal 0 of the block of rows (column 0, row 0 of the warp).
-__device__ __forceinline__ void bin_diagonals(const float* chains, int chain_stride, const uint8_t* bid, float* bins,
-                                              int lane) {
+// One warp's 32 rows x 64 columns of dS, from its chains into its bins: each of
+// the 95 diagonals is the sum of the chains that cross it; those of one bucket
+// are neighbours and are summed by a segmented scan.  bid: the bucket of
+// diagonal 0 of the block (its column 0, its row 0).
+__device__ __forceinline__ void bin_diagonals(const float* chains, const uint8_t* bid, float* bins, int lane) {
+  float s[3];
+  int u[3];
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
     const int y = lane + 32 * k;            // diagonal y - 31
-    float s = 0.0f;
-    int u = 256;
-    if (y < 95) {
-      u = bid[y - 31];
+    u[k] = y < 95 ? bid[y - 31] : 256;
+    s[k] = 0.0f;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int z = y - 16 * c;
-        if (z >= 0 && z < 47) s += chains[c * chain_stride + z];
-      }
+    for (int c = 0; c < kChains; ++c) {
+      const int z = y - 8 * c;
+      if (z >= 0 && z < 39) s[k] += chains[c * kChain + z];
     }
+  }
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const float s2 = __shfl_up_sync(0xffffffffu, s, o);
-      const int u2 = __shfl_up_sync(0xffffffffu, u, o);
-      if (lane >= o && u2 == u) s += s2;
+  for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const float s2 = __shfl_up_sync(0xffffffffu, s[k], o);
+      const int u2 = __shfl_up_sync(0xffffffffu, u[k], o);
+      if (lane >= o && u2 == u[k]) s[k] += s2;
     }
-    const int next = __shfl_down_sync(0xffffffffu, u, 1);
-    if (u < 256 && (lane == 31 || next != u)) bins[u] += s;
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    const int next = __shfl_down_sync(0xffffffffu, u[k], 1);
+    if (u[k] < 256 && (lane == 31 || next != u[k])) bins[u[k]] += s[k];
     __syncwarp();
   }
 }
@@ -748,10 +758,7 @@ __device__ __forceinline__ void bwd_tile(uint32_t tS, const uint8_t* ax, int win
     // over S and dP columns that this thread has read
     if (KEYS) tmem_st16u(tS + c * 16, wp);
     tmem_st16u(tS + 64 + c * 16, wd);
-    if (!KEYS && NEAR && grad) {
-      diagonal_chain(dp, chains + (2 * c) * kChain, lane);
-      diagonal_chain(dp + 16, chains + (2 * c + 1) * kChain, lane);
-    }
+    if (!KEYS && NEAR && grad) diagonal_chains(dp, chains + 4 * c * kChain, lane);
   }
   far_sum += fs.x + fs.y;
 }
@@ -773,7 +780,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   uint8_t* sStAux = sAux + C::kNs * C::kAuxBytes;           // [2]
   float* sBins = reinterpret_cast<float*>(sStAux + C::kSlots * C::kStAux);
   float* sChains = sBins + 8 * kAttnMaxBuckets;
-  uint64_t* bar = reinterpret_cast<uint64_t*>(sChains + 8 * 4 * kChain);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sChains + 8 * kChains * kChain);
   uint64_t *st_full = bar, *st_empty = st_full + C::kSlots, *mv_full = st_empty + C::kSlots,
            *mv_empty = mv_full + C::kNs, *s_full = mv_empty + C::kNs, *p_full = s_full + C::kBuf, *s_free = p_full + C::kBuf,
            *acc_full = s_free + C::kBuf, *acc_free = acc_full + C::kAcc;
@@ -1029,7 +1036,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const uint32_t lo = (uint32_t)((warp & 3) * 32) << 16;
     const float c2 = a.c2;
     float* bins = sBins + warp * kAttnMaxBuckets;
-    float* chains = sChains + warp * 4 * kChain;
+    float* chains = sChains + warp * kChains * kChain;
     const bool want = a.dpart != nullptr;
     if (want)
       for (int u = lane; u < a.buckets; u += 32) bins[u] = 0.0f;
@@ -1108,7 +1115,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[buf]);
-      if (grad && (t.bits & kNear)) bin_diagonals(chains, kChain, a.bid + a.vec_off + t.tile * 64 - row0, bins, lane);
+      if (grad && (t.bits & kNear)) bin_diagonals(chains, a.bid + a.vec_off + t.tile * 64 - row0, bins, lane);
     }
     if (grad) flush();
   }
