@@ -112,8 +112,9 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(const __grid_co
     if (row[k] < rows && lane == 0) {
       const int i = tok[k];
       float* st = a.stats + at[k] * 2 * a.Sp;
-      st[i] = i < a.S ? -a.lse[at[k] * a.S + i] * kAttnLog2e : -INFINITY;
-      st[a.Sp + i] = i < a.S ? -t[k] : 0.0f;
+      const int x = (i >> 6) * 128 + (i & 63);
+      st[x] = i < a.S ? -a.lse[at[k] * a.S + i] * kAttnLog2e : -INFINITY;
+      st[x + 64] = i < a.S ? -t[k] : 0.0f;
     }
   }
 }

@@ -11,7 +11,8 @@
 //   flags  [B or 1][Sp / 64] of each 64 keys: 0 all of maskx is 0, 1 mixed, 2 every key removed
 //   vec    [heads][dirs][4][len] the bias along the diagonals, see bias_at
 //   bid    [len]             the bucket of each of those diagonals
-//   stats  [B * heads][2][Sp] backward: -lse2 (-inf for an empty row and past the end), -D = -(dO.O)
+//   stats  [B * heads][Sp / 64][2][64] backward, per 64 queries: -lse2 (-inf for an empty row and past
+//          the end), then -D = -(dO.O)
 //   dpart  backward: partial sums of the bias table's gradient, zeroed
 // with Sp = the sequence length rounded up to 128.
 #pragma once

@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThr) attn_bwd_kernel(const __grid_constant__ 
   const float* mask = a.maskx + (size_t)mb * a.Sp;
   const int* flags = a.flags + mb * (a.Sp / kAttnFlagKeys);
   const float* nlse = a.stats + (size_t)bh * 2 * a.Sp;
-  const float* nd = nlse + a.Sp;
+  const float* nd = nlse + 64;
   float acc1[4][D / 16] = {}, acc2[4][D / 16] = {};
   const bool grad = !keys && a.dpart;
   if (grad)
@@ -224,11 +224,12 @@ __global__ void __launch_bounds__(kThr) attn_bwd_kernel(const __grid_constant__ 
         const int row = r0 + 4 * ty + i, col = c0 + 4 * tx + j;
         const int qi = keys ? col : row, kj = keys ? row : col;   // both below Sp
         const float bias = vec ? bias_at(a, vec, kj - qi) : 0.0f;
-        const float mk = mask[kj], nl = nlse[qi];
+        const int st = (qi >> 6) * 128 + (qi & 63);
+        const float mk = mask[kj], nl = nlse[st];
         // a removed key, an empty row: p = 0
         const float p = mk == -INFINITY || nl == -INFINITY ? 0.0f : exp2f(fmaf(s[i][j], a.c2, bias + mk) + nl);
         s[i][j] = p;
-        dp[i][j] = p == 0.0f ? 0.0f : p * (dp[i][j] + nd[qi]);
+        dp[i][j] = p == 0.0f ? 0.0f : p * (dp[i][j] + nd[st]);
       }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

@@ -824,7 +824,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const float* vec = a.vec ? bias_copy(a, h, 0, 0) : nullptr;
       const float behind = vec ? vec[a.vec_off - a.sat - 1] : 0.0f, ahead = vec ? vec[a.vec_off + a.sat - 1] : 0.0f;
       const float* stats = a.stats + (size_t)bh * 2 * a.Sp;
-      const float* col = keys ? stats + (lane == 9 ? a.Sp : 0) : a.maskx + (size_t)mb * a.Sp;
       LiveTiles<1> tiles(flags, nm, lane);
       bool mix = false;
       int j = keys ? (flags[2 * ri] == 2 && flags[2 * ri + 1] == 2 ? nm : 0) : tiles.next(0, mix);
@@ -839,12 +838,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           tma_load_4d(st + c * kRegion, keys ? &tk2 : &tq2, &st_full[slot], c * 64, ri * 128, h, b);
           tma_load_4d(st + C::kSt + c * kRegion, keys ? &tv2 : &tdo2, &st_full[slot], c * 64, ri * 128, h, b);
         }
-        if (keys) {
-          bulk_load_1d(row_vec(n), a.maskx + (size_t)mb * a.Sp + ri * 128, 512, &st_full[slot]);
-        } else {
-          bulk_load_1d(row_vec(n), a.stats + (size_t)bh * 2 * a.Sp + ri * 128, 512, &st_full[slot]);
-          bulk_load_1d(row_vec(n) + 128, a.stats + (size_t)bh * 2 * a.Sp + a.Sp + ri * 128, 512, &st_full[slot]);
-        }
+        if (keys) bulk_load_1d(row_vec(n), a.maskx + (size_t)mb * a.Sp + ri * 128, 512, &st_full[slot]);
+        else bulk_load_1d(row_vec(n), stats + ri * 256, 1024, &st_full[slot]);
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
       bool first = true;
@@ -869,30 +864,28 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           }
           if (mix && !keys) t.bits |= kMixed;
         }
-        const bool near = t.bits & kNear, one = !none && (keys || near || (t.bits & kMixed)), two = !none && keys;
+        const bool near = t.bits & kNear, mk = near && !keys || (t.bits & kMixed);
         if (lane == 0 && ok && (ok = wait_bar<kPauseLoad>(&mv_empty[ms], ((g / C::kNs) & 1) ^ 1, err, 303))) {
           *info_of(g) = t;
-          mbar_arrive_expect_tx(&mv_full[ms], (near ? 4 * kRun * 4 : 0) + (one ? 256 : 0) + (two ? 256 : 0) +
-                                                  (none ? 0 : 2 * C::kMv));
+          mbar_arrive_expect_tx(&mv_full[ms], none ? 0 : 2 * C::kMv + (keys ? 512 : 0) + (mk ? 256 : 0) +
+                                                             (near ? 4 * kRun * 4 : 0));
+          if (!none) {
+            uint8_t* ax = sAux + ms * C::kAuxBytes;
+            uint8_t* mv = sMv + ms * 2 * C::kMv;
+            for (int c = 0; c < D / 64; ++c) {
+              tma_load_4d(mv + c * C::kMvRegion, keys ? &tq : &tk, &mv_full[ms], c * 64, j * 64, h, b);
+              tma_load_4d(mv + C::kMv + c * C::kMvRegion, keys ? &tdo : &tv, &mv_full[ms], c * 64, j * 64, h, b);
+            }
+            if (keys) bulk_load_1d(ax + kVecs, stats + j * 128, 512, &mv_full[ms]);
+            if (mk) bulk_load_1d(ax + kVecs, a.maskx + (size_t)mb * a.Sp + j * 64, 256, &mv_full[ms]);
+            if (near)
+              for (int k = 0; k < 4; ++k)
+                bulk_load_1d(ax + k * kWin * 4, bias_copy(a, h, keys ? 1 : 0, k) + x0 - 128 + a.vec_off, kRun * 4,
+                             &mv_full[ms]);
+          }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
-        // a lane per copy
-        uint8_t* ax = sAux + ms * C::kAuxBytes;
-        uint8_t* mv = sMv + ms * 2 * C::kMv;
-        if (lane < 2 * D / 64) {
-          const int c = lane >> 1;
-          if (!none)
-            tma_load_4d(mv + (lane & 1) * C::kMv + c * C::kMvRegion,
-                        lane & 1 ? (keys ? &tdo : &tv) : (keys ? &tq : &tk), &mv_full[ms], c * 64, j * 64, h, b);
-        } else if (lane >= 4 && lane < 8) {
-          if (near)
-            bulk_load_1d(ax + (lane - 4) * kWin * 4, bias_copy(a, h, keys ? 1 : 0, lane - 4) + x0 - 128 + a.vec_off,
-                         kRun * 4, &mv_full[ms]);
-        } else if (lane == 8 || lane == 9) {
-          if (lane == 8 ? one : two) bulk_load_1d(ax + kVecs + (lane - 8) * 256, col + j * 64, 256, &mv_full[ms]);
-        }
-        __syncwarp();
         first = false;
         ++g;
         j = jn;
@@ -1079,8 +1072,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (grad) flush();
         cur = t.item;
         const float* rv = row_vec(cur);
-        add = rv[r];
-        nd = keys ? 0.0f : rv[128 + r];
+        add = rv[keys ? r : (r >> 6) * 128 + (r & 63)];
+        nd = keys ? 0.0f : rv[(r >> 6) * 128 + 64 + (r & 63)];
         grad = want && !keys;
         const int x = (int)(blockIdx.x + (unsigned)cur * gridDim.x) - (keys ? 0 : items);
         const int bh = x / nr, ri = x - bh * nr;
