@@ -181,6 +181,22 @@ size_t layer_workspace_bytes(const tl_layer* layer);
 size_t layer_scratch_bytes(const tl_layer* layer);
 tl_status layer_share_scratch(tl_layer* layer, void* scratch, size_t bytes);
 
+/* Gives the layer's attention a learned relative position bias: scores become
+ * Q K^T / sqrt(d) + table[bucket(j - i), head] + mask (buckets as under
+ * tl_attention below), and layer_backward also writes the table's gradient.
+ * table: (buckets, heads), storage dtype; dtable: the same shape, float32, or
+ * NULL when its gradient is not wanted; overwritten by each layer_backward, or
+ * added to when `accumulate` is not 0 (one table shared by the layers of a
+ * stack: zero it first).  Both are read and written by later calls and must
+ * stay valid; table NULL takes the bias away (the other arguments are ignored).
+ * The layer allocates a workspace of its own for it (TL_ENOMEM).  Discards the
+ * saved activations, and layer_set_options takes the bias away.  TL_EINVAL for
+ * buckets or a distance that tl_attention refuses.  Attention dropout has no
+ * place in these kernels: with attn_dropout > 0 a training-mode forward returns
+ * TL_EUNSUPPORTED (inference is served). */
+tl_status layer_set_position_bias(tl_layer* layer, const void* table, int buckets, int max_distance,
+                                  float* dtable, int accumulate);
+
 /* Text of the last error on this layer ("" if none).  Valid until the next call. */
 const char* layer_last_error(const tl_layer* layer);
 

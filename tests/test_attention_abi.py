@@ -129,3 +129,19 @@ def test_python_calls_refuse_cpu_tensors():
         tlp.clip_grad_norm([q], 1.0)
     with pytest.raises(tlp.TlError):
         tlp.clip_grad_norm([], 1.0)
+
+
+def test_position_bias_arguments(lib):
+    """Refusals that need no device: a null layer, bad buckets and distances."""
+    h = ctypes.c_void_p()
+    assert lib.layer_create(2, 16, 64, 4, 0, 0.0, 0.0, 1, 1, ctypes.byref(h)) == OK
+    f = lib.layer_set_position_bias
+    try:
+        assert f(None, AT, 32, 128, None, 0) == EINVAL
+        assert f(h, None, 0, 0, None, 0) == OK           # nothing to take away
+        for buckets, distance in ((31, 128), (2, 128), (258, 1000), (32, 8), (32, 1 << 21)):
+            assert f(h, AT, buckets, distance, None, 0) == EINVAL
+            assert lib.layer_last_error(h)
+        assert f(h, AT, 32, 128, AT + 1, 0) == EINVAL
+    finally:
+        lib.layer_destroy(h)

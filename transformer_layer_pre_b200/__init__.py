@@ -34,7 +34,7 @@ EXPORTED_SYMBOLS = (
     "tl_profile_read", "tl_launch_count", "tl_bias_grad_noalloc", "tl_gelu_eval", "tl_status_string",
     "tl_pld_theta", "tl_pld_keep_prob", "tl_pld_keep", "tl_gelu_tanh_eval",
     "tl_set_wait_limit_ns", "tl_wait_probe", "layer_scratch_bytes", "layer_share_scratch",
-    "tl_attention_workspace_bytes", "tl_attention_forward", "tl_attention_backward",
+    "layer_set_position_bias", "tl_attention_workspace_bytes", "tl_attention_forward", "tl_attention_backward",
     "tl_clip_workspace_bytes", "tl_clip_grad_norm",
 )
 PROFILE_CLASSES = ("gemm", "attn_fwd", "attn_bwd", "ln_fwd", "ln_bwd", "rowwise")
@@ -144,6 +144,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.tl_set_wait_limit_ns.restype = i
     lib.tl_wait_probe.argtypes = [vp]
     lib.tl_wait_probe.restype = i
+    lib.layer_set_position_bias.argtypes = [vp, vp, i, i, vp, i]
+    lib.layer_set_position_bias.restype = i
     sz, desc, heads = ctypes.c_size_t, ctypes.POINTER(_Attention), ctypes.POINTER(_Heads)
     lib.tl_attention_workspace_bytes.argtypes = [desc, i]
     lib.tl_attention_workspace_bytes.restype = sz
@@ -239,6 +241,27 @@ class Layer:
         self._check(self.lib.layer_backward(self.handle, _ptr(x), _ptr(dy), ctypes.byref(wt), ctypes.byref(gt),
                                             _ptr(dx), _stream(stream)))
         return dx, grads
+
+    def set_position_bias(self, table, max_distance=128, dtable=None, accumulate=False):
+        """Learned relative position bias of the layer's attention: table
+        (buckets, heads) in the layer's dtype (None: no bias), dtable its
+        float32 gradient, written by every backward, or added to with
+        accumulate (one table for several layers).  Both are kept and used by
+        later calls.  Needs attn_dropout 0 in training."""
+        if table is None:
+            self._check(self.lib.layer_set_position_bias(self.handle, None, 0, 0, None, 0))
+            self._bias_ref = None
+            return
+        if table.dim() != 2 or table.shape[1] != self.heads or table.dtype != self.dtype or not table.is_contiguous():
+            _fail("table must be a contiguous (buckets, heads) tensor of the layer's dtype")
+        if dtable is not None and (dtable.shape != table.shape or dtable.dtype != torch.float32
+                                   or dtable.device != table.device or not dtable.is_contiguous()):
+            _fail("dtable must be a contiguous float32 tensor of table's shape on its device")
+        if not table.is_cuda:
+            _fail("table must be on the layer's device")
+        self._check(self.lib.layer_set_position_bias(self.handle, _ptr(table), table.shape[0], max_distance,
+                                                     _ptr(dtable), int(accumulate)))
+        self._bias_ref = (table, dtable)
 
     @property
     def workspace_bytes(self) -> int:

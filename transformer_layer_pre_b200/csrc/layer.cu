@@ -79,6 +79,14 @@ struct tl_layer {
   float* splitk[4] = {nullptr, nullptr, nullptr, nullptr};
   size_t splitk_floats[4] = {0, 0, 0, 0};
   int gemm_err = 0;
+  tl_status attn_err = TL_OK;
+  // relative position bias (table null: none), and the workspace of the
+  // attention entry points that it runs through
+  tl_attention bias = {};
+  float* dtable = nullptr;
+  int dtable_add = 0;
+  void* bias_ws = nullptr;
+  size_t bias_ws_bytes = 0;
 };
 
 namespace {
@@ -126,6 +134,17 @@ void free_buffers(tl_layer* L) {
   L->arena_bytes = 0;
   free_scratch(L);
   L->have_fwd = false;
+}
+
+void free_bias(tl_layer* L) {
+  if (L->bias_ws) {
+    cudaDeviceSynchronize();
+    cudaFree(L->bias_ws);
+  }
+  L->bias_ws = nullptr;
+  L->bias_ws_bytes = 0;
+  L->bias = tl_attention{};
+  L->dtable = nullptr;
 }
 
 struct Carver {
@@ -315,15 +334,46 @@ void bias_grad(tl_layer* L, const void* X, int cols, int slot, float* out, Final
   fin.job[fin.n++] = {part, out, colsum_parts(L->T), cols};
 }
 
+void bias_attn(tl_layer* L, const AttnArgs& a, bool backward, cudaStream_t s);
+
 void attn_fwd(tl_layer* L, const AttnArgs& a, cudaStream_t s) {
+  if (L->bias.bias_table) return bias_attn(L, a, false, s);
   ProfScope p_(PC_ATTN_FWD, s);
   if (attn_tc_supports(L->opt.dtype, a)) attn_tc_fwd_run(L->opt.dtype, a, s);
   else attn_simt_fwd_run(L->opt.dtype, a, s);
 }
 void attn_bwd(tl_layer* L, const AttnArgs& a, cudaStream_t s) {
+  if (L->bias.bias_table) return bias_attn(L, a, true, s);
   ProfScope p_(PC_ATTN_BWD, s);
   if (attn_tc_supports(L->opt.dtype, a)) attn_tc_bwd_run(L->opt.dtype, a, s);
   else attn_simt_bwd_run(L->opt.dtype, a, s);
+}
+
+// Attention with a position bias: the attention entry points on the layer's
+// buffers.  `rows`: tensors of (T, cols) rows, the head at column h * d.
+tl_heads head_view(const tl_layer* L, const void* p) {
+  return {const_cast<void*>(p), (int64_t)L->nh * L->S * L->d, L->d, (int64_t)L->S * L->d};
+}
+tl_heads row_view(const tl_layer* L, const void* p, int cols) {
+  return {const_cast<void*>(p), (int64_t)L->S * cols, cols, L->d};
+}
+void bias_attn(tl_layer* L, const AttnArgs& a, bool backward, cudaStream_t s) {
+  const size_t es = dtype_size(L->opt.dtype);
+  tl_attention c = L->bias;
+  c.mask = a.mask;
+  const tl_heads q = head_view(L, a.q), k = head_view(L, a.k), v = head_view(L, a.v), o = row_view(L, a.ctx, L->H);
+  tl_status st;
+  if (!backward) {
+    st = tl_attention_forward(&c, &q, &k, &v, &o, a.lse, L->bias_ws, L->bias_ws_bytes, s);
+  } else {
+    const tl_heads dout = row_view(L, a.dctx, L->H);
+    char* g = static_cast<char*>(a.dqkv);
+    const tl_heads dq = row_view(L, g, 3 * L->H), dk = row_view(L, g + L->H * es, 3 * L->H),
+                   dv = row_view(L, g + 2 * L->H * es, 3 * L->H);
+    st = tl_attention_backward(&c, &q, &k, &v, &o, &dout, a.lse, &dq, &dk, &dv, L->dtable, L->dtable_add, L->bias_ws,
+                               L->bias_ws_bytes, s);
+  }
+  if (st != TL_OK) L->attn_err = st;
 }
 
 AttnArgs attn_args(tl_layer* L, const float* mask) {
@@ -408,6 +458,7 @@ tl_status layer_set_options(tl_layer* L, const tl_options* o) {
   char* shared = (L->scratch && !L->scratch_owned) ? L->scratch : nullptr;
   const size_t shared_bytes = shared ? L->scratch_bytes : 0;
   free_buffers(L);
+  free_bias(L);
   L->opt = *o;
   L->opt.training = o->training ? 1 : 0;
   L->opt.gelu_tanh = o->gelu_tanh ? 1 : 0;
@@ -435,7 +486,45 @@ tl_status layer_get_options(const tl_layer* L, tl_options* o) {
 }
 
 size_t layer_workspace_bytes(const tl_layer* L) {
-  return L ? L->arena_bytes + (L->scratch_owned ? L->scratch_bytes : 0) : 0;
+  return L ? L->arena_bytes + (L->scratch_owned ? L->scratch_bytes : 0) + L->bias_ws_bytes : 0;
+}
+
+tl_status layer_set_position_bias(tl_layer* L, const void* table, int buckets, int max_distance, float* dtable,
+                                  int accumulate) {
+  if (!L) return TL_EINVAL;
+  L->err.clear();
+  if (!table) {
+    free_bias(L);
+    L->have_fwd = false;
+    return TL_OK;
+  }
+  tl_attention c = {};
+  c.dtype = L->opt.dtype;
+  c.batch = L->B; c.seq = L->S; c.heads = L->nh; c.head_dim = L->d;
+  c.bias_table = table; c.buckets = buckets; c.max_distance = max_distance;
+  // the workspace is the same with and without a mask but for its rows
+  static const float kMask = 0.0f;
+  c.mask = &kMask;
+  const size_t need = tl_attention_workspace_bytes(&c, 1);
+  if (!need) return fail(L, TL_EINVAL, "position bias: buckets even, 4 to 256, buckets/4 < max_distance <= 2^20");
+  if (reinterpret_cast<uintptr_t>(dtable) & 3) return fail(L, TL_EINVAL, "dtable must be 4-byte aligned");
+  c.mask = nullptr;
+  tl_status st = ensure_buffers(L);
+  if (st != TL_OK) return st;
+  if (L->bias_ws_bytes < need) {
+    free_bias(L);
+    if (cudaMalloc(&L->bias_ws, need) != cudaSuccess) {
+      cudaGetLastError();
+      L->bias_ws = nullptr;
+      return fail(L, TL_ENOMEM, "cudaMalloc of the position bias workspace failed");
+    }
+    L->bias_ws_bytes = need;
+  }
+  L->bias = c;
+  L->dtable = dtable;
+  L->dtable_add = accumulate ? 1 : 0;
+  L->have_fwd = false;
+  return TL_OK;
 }
 
 size_t layer_scratch_bytes(const tl_layer* L) { return L ? scratch_size(L) : 0; }
@@ -460,6 +549,7 @@ const char* layer_last_error(const tl_layer* L) { return L ? L->err.c_str() : "n
 void layer_destroy(tl_layer* L) {
   if (!L) return;
   free_buffers(L);
+  free_bias(L);
   delete L;
 }
 
@@ -482,6 +572,8 @@ tl_status layer_forward(tl_layer* L, const void* x, const float* mask, const tl_
   cudaStream_t s = (cudaStream_t)stream;
   const int dt = L->opt.dtype, T = L->T, H = L->H, F = L->F;
   const bool train = L->opt.training != 0;
+  if (train && L->bias.bias_table && L->pa > 0.0f)
+    return fail(L, TL_EUNSUPPORTED, "a position bias needs attn_dropout 0 in training");
   L->have_fwd = false;
   L->drop_seed = L->seed;
   L->drop_offset = L->opt.philox_offset;
@@ -517,7 +609,7 @@ tl_status layer_forward(tl_layer* L, const void* x, const float* mask, const tl_
   // head and token, LN1 itself became compute-bound: at S = 512 it took 58
   // instead of 27 us while the attention forward saved 14 us, so there the
   // forward's helper warps draw them.)
-  const bool attn_bits = aa.drop.thr && L->akeep && L->S <= 128 && attn_tc_supports(dt, aa);
+  const bool attn_bits = !L->bias.bias_table && aa.drop.thr && L->akeep && L->S <= 128 && attn_tc_supports(dt, aa);
   if (L->pre_ln) {
     AttnKeepGen ak = {};
     if (attn_bits) {
@@ -572,6 +664,11 @@ tl_status layer_forward(tl_layer* L, const void* x, const float* mask, const tl_
   if (L->gemm_err) {
     L->gemm_err = 0;
     return fail(L, TL_ECUDA, "a GEMM operand could not be described to the TMA unit");
+  }
+  if (L->attn_err != TL_OK) {
+    st = L->attn_err;
+    L->attn_err = TL_OK;
+    return fail(L, st, "attention with a position bias failed");
   }
   L->mask = mask;
   L->have_fwd = train;
@@ -692,7 +789,7 @@ tl_status layer_backward(tl_layer* L, const void* x, const void* dy, const tl_we
     gemm2(L, wdesc(L, 2, &fin, H, H, T, L->da, H, L->ctx, H), ewo,           // dWo = dA^T ctx
           gdesc(L, T, H, H, L->da, H, true, w->wo, H, false), edc, s);     // dctx = dA Wo
     AttnArgs aa = attn_args(L, L->mask);
-    const bool fused_dbqkv = attn_tc_supports(dt, aa) && attn_tc_fuses_colsum(dt, aa);
+    const bool fused_dbqkv = !L->bias.bias_table && attn_tc_supports(dt, aa) && attn_tc_fuses_colsum(dt, aa);
     if (fused_dbqkv) {
       aa.colsum = sink(dbqkv_slot, g->bqkv);
       aa.colsum_acc = relaxed ? 1 : 0;
@@ -738,6 +835,11 @@ tl_status layer_backward(tl_layer* L, const void* x, const void* dy, const tl_we
   }
   (void)es;
   st = check_cuda(L, "layer_backward");
+  if (st == TL_OK && L->attn_err != TL_OK) {
+    st = L->attn_err;
+    L->attn_err = TL_OK;
+    return fail(L, st, "attention with a position bias failed");
+  }
   if (st == TL_OK && L->gemm_err) {
     L->gemm_err = 0;
     return fail(L, TL_ECUDA, "a GEMM operand could not be described to the TMA unit");

@@ -23,13 +23,25 @@ exchange=True)` averages each layer's gradients over the ranks as soon as
 that layer's backward is enqueued, on a side stream, so the collective
 overlaps the backward of the layers below it (one bucket per layer, the
 layer's flat float32 gradient buffer).
+
+A learned relative position bias (`set_position_bias`) is one table shared by
+every layer's attention; its gradient is the sum over the layers.  The global
+gradient norm and clipping (`clip_grad_norm`) run over the flat buffers of the
+layers that ran, and the table's gradient, after the exchange.
 """
 from __future__ import annotations
 
 import torch
 
-from . import Layer, pld_keep, pld_theta
+from . import Layer, clip_grad_norm, pld_keep, pld_theta
 from .dp import FlatGrads, GradExchanger
+
+
+class _TableGrad:
+    """The shared bias table's gradient, as the exchange takes a buffer."""
+
+    def __init__(self, table: torch.Tensor):
+        self.flat = torch.zeros(table.shape, dtype=torch.float32, device=table.device)
 
 
 class EncoderStack:
@@ -63,6 +75,36 @@ class EncoderStack:
         self.inputs: list = [None] * num_layers
         self.dys: list = [None] * num_layers
         self.keep: list = [True] * num_layers
+        self.heads = heads
+        self.table_grad: _TableGrad | None = None
+
+    def set_position_bias(self, table, max_distance: int = 128) -> None:
+        """One relative position bias table, (buckets, heads) in the stack's
+        dtype, for the attention of every layer (None: no bias); its float32
+        gradient is `position_bias_grad`, overwritten by each backward.  Needs
+        attn_dropout 0 in training."""
+        self.table_grad = None if table is None else _TableGrad(table)
+        for layer in self.layers:
+            if table is None:
+                layer.set_position_bias(None)
+            else:
+                layer.set_position_bias(table, max_distance, self.table_grad.flat, accumulate=True)
+
+    @property
+    def position_bias_grad(self):
+        """Gradient of the shared table, or None without one."""
+        return None if self.table_grad is None else self.table_grad.flat
+
+    def clip_grad_norm(self, max_norm: float, stream=None) -> torch.Tensor:
+        """Scales the gradients of the last backward in place so that their
+        global norm is at most max_norm (see the package's clip_grad_norm);
+        returns the norm before, a (1,) float32 tensor on the device."""
+        grads = [g.flat for g, keep in zip(self.grads, self.keep) if keep]
+        if self.table_grad is not None:
+            grads.append(self.table_grad.flat)
+        if not grads:
+            return torch.zeros(1, dtype=torch.float32, device=self.device)
+        return clip_grad_norm(grads, max_norm, stream=stream)
 
     def set_step(self, step: int) -> None:
         """Dropout masks of global step `step`: layer l draws with
@@ -103,6 +145,12 @@ class EncoderStack:
         out = [None] * self.num_layers
         ex = exchange if isinstance(exchange, GradExchanger) else (GradExchanger() if exchange else None)
         g = dy
+        if self.table_grad is not None:
+            if stream is None:
+                self.table_grad.flat.zero_()
+            else:
+                with torch.cuda.stream(stream):
+                    self.table_grad.flat.zero_()
         for l in reversed(range(self.num_layers)):
             self.dys[l] = g
             if not self.keep[l]:
@@ -113,6 +161,8 @@ class EncoderStack:
             if ex is not None:
                 ex.submit(self.grads[l], stream)
         if ex is not None:
+            if self.table_grad is not None:
+                ex.submit(self.table_grad, stream)
             ex.finish(stream)
         return g, out
 
