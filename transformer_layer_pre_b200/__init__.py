@@ -8,6 +8,7 @@ LibraryMissing is raised.
 
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -445,20 +446,22 @@ def clip_grad_norm(grads, max_norm, out=None, stream=None):
     if index < 0 or code is None:
         _fail("gradients must be float32, float16 or bfloat16 tensors on a CUDA device")
     every = grads if out is None else grads + outs
-    if (any([t.dtype is not dtype for t in every]) or set(map(torch.Tensor.get_device, every)) != {index}
+    if ({t.dtype for t in every} != {dtype} or set(map(torch.Tensor.get_device, every)) != {index}
             or not all(map(torch.Tensor.is_contiguous, every))):
         _fail("gradients and outputs must be contiguous tensors of one dtype and device")
     sizes = list(map(torch.Tensor.numel, grads))
-    src = dst = (ctypes.c_void_p * n)(*map(torch.Tensor.data_ptr, grads))
+    # 64-bit words in the lists' own memory: a ctypes array of n costs more than the launch
+    src = dst = array.array("Q", map(torch.Tensor.data_ptr, grads))
     if out is not None:
         if list(map(torch.Tensor.numel, outs)) != sizes:
             _fail("an output for every gradient, of its size")
-        dst = (ctypes.c_void_p * n)(*map(torch.Tensor.data_ptr, outs))
+        dst = array.array("Q", map(torch.Tensor.data_ptr, outs))
+    count = array.array("Q", sizes)
     with _Call(index, stream) as call:
         norm = grads[0].new_empty(1, dtype=torch.float32)
         ws = norm.new_empty(lib.tl_clip_workspace_bytes(n), dtype=torch.uint8)
-        _check(lib.tl_clip_grad_norm(code, n, src, dst, (ctypes.c_uint64 * n)(*sizes), max_norm, norm.data_ptr(),
-                                     ws.data_ptr(), ws.numel(), call.raw))
+        _check(lib.tl_clip_grad_norm(code, n, src.buffer_info()[0], dst.buffer_info()[0], count.buffer_info()[0],
+                                     max_norm, norm.data_ptr(), ws.data_ptr(), ws.numel(), call.raw))
     return norm
 
 
