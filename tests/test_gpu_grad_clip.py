@@ -83,6 +83,15 @@ def test_not_finite(bad):
         assert math.isnan(float(flat[4321])) and int((flat == 0).sum()) == flat.numel() - 1
 
 
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+def test_measuring_only_changes_nothing(bad):
+    grads, flat = _make("f32", [5000, 77])
+    flat[4321] = bad
+    keep = flat.clone()
+    norm = tlp.clip_grad_norm(grads, math.inf)
+    assert not math.isfinite(float(norm)) and torch.equal(flat.view(torch.int32), keep.view(torch.int32))
+
+
 def test_graph_and_streams_repeat_bitwise():
     sets = [_make("f32", [200001, 5, 64], seed=s) for s in range(2)]
     want = []

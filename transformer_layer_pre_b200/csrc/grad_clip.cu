@@ -18,7 +18,12 @@
 // exceeds L2 is read twice and written once.
 #include <cuda_runtime.h>
 
+#include <math.h>
+
 #include <algorithm>
+#include <memory>
+#include <new>
+#include <utility>
 
 #include "../../include/tlp.h"
 #include "kernels.h"
@@ -155,7 +160,8 @@ __global__ void __launch_bounds__(kClipThreads)
   const double norm = sqrt(block_sum_f64(acc, red));
   if (blockIdx.x == 0 && threadIdx.x == 0 && norm_out) *norm_out = (float)norm;
   const double ratio = max_norm / (norm + 1e-6);
-  const float f = ratio > 1.0 ? 1.0f : (float)ratio;   // NaN stays NaN
+  // NaN stays NaN; without a limit there is nothing to scale, whatever the norm
+  const float f = ratio > 1.0 || max_norm == INFINITY ? 1.0f : (float)ratio;
   if (in_place && f == 1.0f) return;
   for (uint64_t k = blockIdx.x; k < l.chunks; k += gridDim.x) {
     const uint64_t c = l.chunks - 1 - k;
@@ -244,6 +250,37 @@ void run_t(int dt, int count, const void* const* in, void* const* out, const uin
   else run<T, kCapLarge>(dt, count, in, out, n, max_norm, norm, in_place, ws, s);
 }
 
+// Whether no output shares memory with another tensor of the call (its own
+// input at the same address apart).
+bool separate(int count, const void* const* in, void* const* out, const uint64_t* n, uint64_t es) {
+  using Range = std::pair<uintptr_t, uintptr_t>;
+  constexpr int kStack = 256;
+  Range few[kStack];
+  std::unique_ptr<Range[]> many(count > kStack ? new (std::nothrow) Range[count] : nullptr);
+  if (count > kStack && !many) return false;
+  Range* r = many ? many.get() : few;
+  int m = 0;
+  bool sorted = true;
+  for (int i = 0; i < count; ++i) {
+    if (n[i] == 0) continue;
+    const uintptr_t p = reinterpret_cast<uintptr_t>(out[i]);
+    r[m] = {p, p + n[i] * es};
+    sorted = sorted && (m == 0 || r[m - 1].first <= p);
+    ++m;
+  }
+  if (!sorted) std::sort(r, r + m);
+  for (int i = 1; i < m; ++i)
+    if (r[i].first < r[i - 1].second) return false;
+  for (int i = 0; i < count; ++i) {
+    if (n[i] == 0 || in[i] == out[i]) continue;
+    const uintptr_t b = reinterpret_cast<uintptr_t>(in[i]), e = b + n[i] * es;
+    // the outputs are in order and apart: the first that ends behind the input's start
+    const Range* x = std::upper_bound(r, r + m, b, [](uintptr_t at, const Range& y) { return at < y.second; });
+    if (x != r + m && x->first < e) return false;
+  }
+  return true;
+}
+
 }  // namespace
 }  // namespace tlp
 
@@ -271,6 +308,7 @@ tl_status tl_clip_grad_norm(int dtype, int count, const void* const* in, void* c
     if ((reinterpret_cast<uintptr_t>(in[i]) | reinterpret_cast<uintptr_t>(out[i])) & (es - 1)) return TL_EINVAL;
     if (in[i] != out[i]) in_place = 0;
   }
+  if (!separate(count, in, out, n, es)) return TL_EINVAL;
   if (cudaPeekAtLastError() != cudaSuccess) {
     cudaGetLastError();
     return TL_ECUDA;
