@@ -303,7 +303,9 @@ tl_status tl_bias_grad_noalloc(int dtype, const void* dz, int rows, int cols, fl
  * the head_dim entries of one head are contiguous.  data is 16-byte aligned,
  * and the strides of every dimension of more than one entry are multiples of
  * 16 bytes and at least head_dim (those of one entry are ignored).  Outputs
- * must not overlap anything else; elements between their rows are left alone.
+ * must not overlap anything else, and each of an output's dimensions steps over
+ * all of those with smaller strides (TL_EINVAL); elements between their rows
+ * are left alone.
  * lse: (batch, heads, seq) float32, dense.  bias_table: (buckets, heads),
  * dense, storage dtype; dtable: the same shape, float32, overwritten, or added
  * to when `accumulate` is not 0; NULL when its gradient is not wanted.
@@ -339,11 +341,13 @@ tl_status tl_attention_backward(const tl_attention* desc, const tl_heads* q, con
  *   out  = g * min(1, max_norm / (norm + 1e-6)), rounded to the dtype
  * in[i], out[i]: n[i] elements each, any alignment that the type has; out[i]
  * is in[i] itself (in place: where the norm is within the limit nothing is
- * written) or memory that no other tensor of the call overlaps.  norm: one
+ * written) or memory that no other tensor of the call overlaps (TL_EINVAL:
+ * a gradient listed twice has no meaning here).  norm: one
  * float32 on the device (required).  Squares and their sum are float64, in a
  * fixed order: bitwise reproducible.  A gradient that is not finite makes the
  * norm infinite or NaN and the outputs follow the formula (0 or NaN).
- * max_norm >= 0; +inf measures only (in place).  The pointer lists are read
+ * max_norm >= 0; +inf measures only (factor 1, whatever the norm).  The
+ * pointer lists are read
  * before the call returns.  workspace: tl_clip_workspace_bytes(count) bytes,
  * 8-byte aligned, not kept from call to call; calls that may overlap on the
  * GPU need one each. */

@@ -91,6 +91,22 @@ def test_other_pointers_refused(lib):
     assert b(none, q, k, v, o, do, AT, dq, dk, dv, AT, 0, AT, need, None) == EINVAL   # a table gradient without a table
 
 
+@pytest.mark.parametrize("shared", [
+    dict(token=64),                      # rows over the heads of their neighbours
+    dict(batch=192),                     # sequences over one another
+    dict(head=33 * 192 - 128, token=192),
+])
+def test_outputs_over_themselves_refused(lib, shared):
+    d = _desc()
+    need = lib.tl_attention_workspace_bytes(d, 1)
+    q, k, v, o, do, dq, dk, dv = (_view(AT * (i + 1)) for i in range(8))
+    assert lib.tl_attention_forward(d, q, k, v, _view(AT * 4, **shared), AT, AT, need, None) == EINVAL
+    for i in range(3):
+        outs = [dq, dk, dv]
+        outs[i] = _view(AT * (6 + i), **shared)
+        assert lib.tl_attention_backward(d, q, k, v, o, do, AT, *outs, AT, 0, AT, need, None) == EINVAL
+
+
 def test_workspace_grows_with_the_call(lib):
     n = lib.tl_attention_workspace_bytes(_desc(), 0)
     assert 0 < n < lib.tl_attention_workspace_bytes(_desc(), 1)
@@ -112,6 +128,20 @@ def _clip(lib, dtype=0, count=1, src=(AT,), dst=(AT,), n=(8,), limit=1.0, norm=A
 ])
 def test_clip_refusals(lib, bad):
     assert _clip(lib, **bad) == EINVAL
+
+
+@pytest.mark.parametrize("many", [2, 300])
+@pytest.mark.parametrize("dst", [
+    (AT, AT),                            # one gradient twice
+    (AT, AT + 28),                       # the last value of one is the first of the other
+    (3 * AT, AT),                        # over another input
+    (3 * AT, AT + 32 - 4), (AT + 4, 3 * AT), (3 * AT, 3 * AT),
+])
+def test_clip_outputs_that_overlap_refused(lib, dst, many):
+    src = (AT, dst[1] if dst[0] == AT else 2 * AT)
+    far = tuple((5 + i) * AT for i in range(many - 2))
+    assert _clip(lib, count=many, src=src + far, dst=dst + far, n=(8,) * many) == EINVAL
+    assert _clip(lib, count=many, src=far + src, dst=far + dst, n=(8,) * many) == EINVAL
 
 
 def test_clip_workspace(lib):

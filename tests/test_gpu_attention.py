@@ -254,3 +254,22 @@ def test_python_refusals():
             f()
             pytest.fail(f"call {i} was taken")
     tlp.device_check()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_small_probabilities_of_a_long_row(dtype):
+    """Equal scores: P = 1/seq everywhere (111.5 of float16's smallest steps, so P itself is off by 2^-8 in it), and with
+    dO = 1 every dV is 1.  Bound: P and dV rounded to storage, half a step each; a float32 sum of seq / 16 products that
+    each lose less than one last place, 2^-23; 2^-18 for lse (half a last place of 11.9, doubled by the change of base)."""
+    s, dt = 150469, DT[dtype]
+    g = torch.Generator(device="cuda").manual_seed(7)
+    k = torch.randn(1, s, 1, 8, generator=g, device="cuda").to(dt)
+    v = torch.randn(1, s, 1, 8, generator=g, device="cuda").to(dt)
+    q, do = torch.zeros_like(k), torch.ones_like(k)
+    o, lse = tlp.attention_forward(q, k, v)
+    dq, dk, dv, _ = tlp.attention_backward(q, k, v, o, lse, do)
+    tlp.device_check()
+    u = torch.finfo(dt).eps / 2
+    assert float((lse.double() - math.log(s)).abs().max()) <= 2.0 ** -18
+    assert float((dv.double() - 1).abs().max()) <= 2 * u + s / 16 * 2.0 ** -23 + 2.0 ** -18
+    assert bool((dk == 0).all()) and bool(torch.isfinite(dq).all())

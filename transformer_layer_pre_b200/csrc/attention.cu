@@ -113,8 +113,10 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(const __grid_co
       const int i = tok[k];
       float* st = a.stats + at[k] * 2 * a.Sp;
       const int x = (i >> 6) * 128 + (i & 63);
-      st[x] = i < a.S ? -a.lse[at[k] * a.S + i] * kAttnLog2e : -INFINITY;
-      st[x + 64] = i < a.S ? -t[k] : 0.0f;
+      constexpr float up = sizeof(T) == 2 ? kAttnPUp : 1.0f, up2 = sizeof(T) == 2 ? 8.0f : 0.0f;   // and its log2
+      static_assert(kAttnPUp == 256.0f, "up2 is its logarithm");
+      st[x] = i < a.S ? up2 - a.lse[at[k] * a.S + i] * kAttnLog2e : -INFINITY;
+      st[x + 64] = i < a.S ? -t[k] * (1.0f / up) : 0.0f;
     }
   }
 }
@@ -214,6 +216,20 @@ bool view_ok(const tl_heads* v, int dt, int B, int S, int nh, int d) {
   const int n[3] = {B, S, nh};
   for (int i = 0; i < 3; ++i)
     if (n[i] > 1 && (st[i] < d || st[i] % per != 0 || st[i] >= (1ll << 36))) return false;
+  return true;
+}
+
+// Whether no two entries of an output share memory: sorted by stride, every
+// dimension steps over the whole of the ones inside it.
+bool disjoint(const tl_heads* v, int B, int S, int nh, int d) {
+  struct { int64_t stride; int n; } x[3] = {{v->batch, B}, {v->token, S}, {v->head, nh}};
+  std::sort(x, x + 3, [](const auto& l, const auto& r) { return l.stride < r.stride; });
+  int64_t span = d;
+  for (const auto& e : x) {
+    if (e.n == 1) continue;
+    if (e.stride < span) return false;
+    span += e.stride * (e.n - 1);
+  }
   return true;
 }
 
@@ -320,6 +336,7 @@ tl_status tl_attention_forward(const tl_attention* c, const tl_heads* q, const t
   for (const tl_heads* t : all)
     if (!view_ok(t, c->dtype, a.B, a.S, a.nh, a.d)) return TL_EINVAL;
   if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3) || same(o, q) || same(o, k) || same(o, v)) return TL_EINVAL;
+  if (!disjoint(o, a.B, a.S, a.nh, a.d)) return TL_EINVAL;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < need) return TL_EINVAL;
   if (cudaGetLastError() != cudaSuccess) return TL_ECUDA;
   a.q = view(q, a.B, a.S, a.nh, a.d);
@@ -347,9 +364,11 @@ tl_status tl_attention_backward(const tl_attention* c, const tl_heads* q, const 
   const tl_heads* all[8] = {q, k, v, o, dout, dq, dk, dv};
   for (const tl_heads* t : all)
     if (!view_ok(t, c->dtype, a.B, a.S, a.nh, a.d)) return TL_EINVAL;
-  for (int i = 5; i < 8; ++i)
+  for (int i = 5; i < 8; ++i) {
+    if (!disjoint(all[i], a.B, a.S, a.nh, a.d)) return TL_EINVAL;
     for (int j = 0; j < i; ++j)
       if (same(all[i], all[j])) return TL_EINVAL;
+  }
   if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3)) return TL_EINVAL;
   if (dtable && (!c->bias_table || (reinterpret_cast<uintptr_t>(dtable) & 3))) return TL_EINVAL;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < need) return TL_EINVAL;

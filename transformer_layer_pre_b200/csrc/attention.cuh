@@ -12,7 +12,7 @@
 //   vec    [heads][dirs][4][len] the bias along the diagonals, see bias_at
 //   bid    [len]             the bucket of each of those diagonals
 //   stats  [B * heads][Sp / 64][2][64] backward, per 64 queries: -lse2 (-inf for an empty row and past
-//          the end), then -D = -(dO.O)
+//          the end), then -D = -(dO.O); for 16-bit storage log2(kAttnPUp) - lse2 and -D / kAttnPUp
 //   dpart  backward: partial sums of the bias table's gradient, zeroed
 // with Sp = the sequence length rounded up to 128.
 #pragma once
@@ -29,6 +29,7 @@ constexpr float kAttnLn2 = 0.6931471805599453f;
 constexpr float kAttnMasked = -1e30f;      // a mask value at or below this removes the key
 constexpr int kAttnMaxBuckets = 256;
 constexpr int kAttnFlagKeys = 64;
+constexpr float kAttnPUp = 256.0f;         // 16-bit storage, backward: the factor that P is held at (attention_tc.cu)
 
 // A (batch, token, head, dim) tensor: element strides, dim contiguous.
 struct AttnView {

@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
       mbar_init(&v_full[i], 1), mbar_init(&v_empty[i], 1);
     }
     for (int i = 0; i < C::kAux; ++i) mbar_init(&aux_full[i], 1), mbar_init(&aux_empty[i], 5);
-    mbar_init(s_full, 1);
+    mbar_init(s_full, 2);
     mbar_init(p_full, 4);
     mbar_init(pv_done, 1);
     fence_barrier_init();
@@ -386,6 +386,7 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
           if (t.tile < 0) {
             // nothing to multiply: the phases go on
             mbar_arrive(s_full);
+            mbar_arrive(s_full);
             if (!(ok = wait_bar<0>(p_full, g & 1, err, 211))) break;
             mbar_arrive(pv_done);
             break;
@@ -399,6 +400,7 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
             mma_f16(tmem, dq + (kk >> 2) * (kRegion >> 4) + (kk & 3) * 2,
                     dk + ks * (C::kKvBytes >> 4) + (kk >> 2) * (C::kKvRegion >> 4) + (kk & 3) * 2, id_s, kk > 0);
           mma_commit(s_full);
+          mbar_arrive(s_full);   // orders what this thread waited for; the commit, the products
           mma_commit(&k_empty[ks]);
           // what the next tile needs, ahead of the wait for P (an item's first
           // tile waits for the rows of the item before)
@@ -608,7 +610,11 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
 // other did not need).  P and dS
 // (rounded to the storage type, at most half a step) overwrite S and dP in
 // TMEM and are the A operands of the second pair of products from there, so
-// they never touch shared memory.
+// they never touch shared memory.  P is held kAttnPUp times too large: the
+// probabilities of a long row (1/S each) then stay clear of float16's
+// subnormals, whose rounding is absolute, up to S = 2^22.  The factor comes with
+// -lse2, leaves dS through the product dP / kAttnPUp - D / kAttnPUp, and dV as it
+// is written out; all of it is exact.
 // TMEM: per softmax group S, dP (64 columns each); from 256 on the sums, two
 // sets of them for D = 64, so the next item starts while one is written out.
 constexpr int kRun = 192, kWin = 200;           // diagonals of a 128 x 64 tile, floats of a window copy
@@ -739,8 +745,8 @@ __device__ __forceinline__ void bwd_tile(uint32_t tS, const uint8_t* ax, int win
       const float2 x0 = __ffma2_rn(make_float2(s[e], s[e + 1]), f2(c2), add0);
       const float2 x1 = __ffma2_rn(make_float2(s[e + 2], s[e + 3]), f2(c2), add1);
       const float2 p0 = make_float2(ex2f(x0.x), ex2f(x0.y)), p1 = make_float2(ex2f(x1.x), ex2f(x1.y));
-      const float2 d0 = __fmul2_rn(p0, __fadd2_rn(make_float2(dp[e], dp[e + 1]), nd0));
-      const float2 d1 = __fmul2_rn(p1, __fadd2_rn(make_float2(dp[e + 2], dp[e + 3]), nd1));
+      const float2 d0 = __fmul2_rn(p0, __ffma2_rn(make_float2(dp[e], dp[e + 1]), f2(1.0f / kAttnPUp), nd0));
+      const float2 d1 = __fmul2_rn(p1, __ffma2_rn(make_float2(dp[e + 2], dp[e + 3]), f2(1.0f / kAttnPUp), nd1));
       if (KEYS) {
         wp[e / 2] = pack2<T>(p0.x, p0.y);
         wp[e / 2 + 1] = pack2<T>(p1.x, p1.y);
@@ -790,7 +796,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   int* err = g_attention_err;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kSlots; ++i) mbar_init(&st_full[i], 1), mbar_init(&st_empty[i], 1);
-    for (int i = 0; i < C::kBuf; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 4), mbar_init(&s_free[i], 1);
+    for (int i = 0; i < C::kBuf; ++i) mbar_init(&s_full[i], 2), mbar_init(&p_full[i], 4), mbar_init(&s_free[i], 1);
     for (int i = 0; i < C::kNs; ++i) mbar_init(&mv_full[i], 1), mbar_init(&mv_empty[i], 1);
     for (int i = 0; i < C::kAcc; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_free[i], 4);
     fence_barrier_init();
@@ -918,6 +924,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (t.tile < 0) {
           if (t.bits & kEnd) ++ends;
           mbar_arrive(&s_full[w]);
+          mbar_arrive(&s_full[w]);
           continue;
         }
         tc_fence_after();
@@ -933,6 +940,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           mma_f16(tS + 64, a2 + (kk >> 2) * (kRegion >> 4) + (kk & 3) * 2,
                   b2 + (kk >> 2) * (C::kMvRegion >> 4) + (kk & 3) * 2, id, kk > 0);
         mma_commit(&s_full[w]);
+        mbar_arrive(&s_full[w]);   // orders what this thread waited for; the commit, the products
       }
     }
   } else if (warp == 14) {
@@ -986,7 +994,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       uint8_t* st = sSt + slot * 2 * C::kSt;
 #pragma unroll 1
       for (int q = 0; q < (keys ? 2 : 1); ++q) {
-        const float f = q == 0 ? a.scale : 1.0f;
+        const float f = q == 0 ? a.scale : 1.0f / kAttnPUp;
         uint8_t* out = st + q * C::kSt;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
