@@ -154,7 +154,7 @@ template <typename T, int G>
 void prep(const AttnOp& a, bool backward, cudaStream_t s) {
   const int nmask = a.mask_seqs * ((a.Sp + kPrepThreads - 1) / kPrepThreads);
   const int nvec = a.vec ? a.nh * ((a.vec_len + kPrepThreads - 1) / kPrepThreads) : 0;
-  const int nzero = a.dpart ? 64 : 0;
+  const int nzero = backward && a.dpart ? 64 : 0;
   const long long rows = backward ? (long long)a.B * a.Sp * a.nh : 0;
   constexpr int per = kPrepRows * (kPrepThreads / G);
   const int nrow = (int)((rows + per - 1) / per);
@@ -288,10 +288,11 @@ tl_status plan(const tl_attention* c, bool backward, char* base, AttnOp& a, size
     a.bid = (uint8_t*)(base + take(off, a.vec_len));
   }
   if (backward) {
-    a.stats = (float*)(base + take(off, (size_t)a.B * a.nh * 2 * a.Sp * 4));
+    const bool one = attn_one_tile(c->dtype, a.S, a.d);
+    if (!one) a.stats = (float*)(base + take(off, (size_t)a.B * a.nh * 2 * a.Sp * 4));
     if (c->bias_table) {
-      // one row per item of 64 queries (float32), or per softmax warp of one of 128
-      a.ditems = c->dtype == TL_F32 ? (a.S + 63) / 64 : a.Sp / 128 * 8;
+      // one row per item of 64 queries (float32), per softmax warp of one of 128, or per (sequence, head)
+      a.ditems = c->dtype == TL_F32 ? (a.S + 63) / 64 : one ? 1 : a.Sp / 128 * 8;
       a.dpart = (float*)(base + take(off, (size_t)a.B * a.nh * a.ditems * a.buckets * 4));
     }
   }
@@ -302,6 +303,8 @@ tl_status plan(const tl_attention* c, bool backward, char* base, AttnOp& a, size
 bool same(const tl_heads* x, const tl_heads* y) { return x->data == y->data; }
 
 }  // namespace
+
+bool attn_one_tile(int dt, int seq, int head_dim) { return dt != DT_F32 && seq <= 128 && head_dim <= 64; }
 
 void attn_prep_run(int dt, const AttnOp& a, bool backward, cudaStream_t s) {
   if (dt == DT_F32) prep_t<float>(a, backward, s);
@@ -387,7 +390,8 @@ tl_status tl_attention_backward(const tl_attention* c, const tl_heads* q, const 
   if (!dtable) a.dpart = nullptr;
   cudaStream_t s = (cudaStream_t)stream;
   ProfScope p_(PC_ATTN_BWD, s);
-  attn_prep_run(c->dtype, a, true, s);
+  // one tile per sequence and head: its kernel forms D itself and writes every row of dpart
+  attn_prep_run(c->dtype, a, !attn_one_tile(c->dtype, a.S, a.d), s);
   bool ok = true;
   if (c->dtype == TL_F32) attention_f32_bwd_run(a, s);
   else ok = attention_tc_bwd_run(c->dtype, a, s);

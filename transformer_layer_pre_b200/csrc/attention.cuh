@@ -73,6 +73,9 @@ __device__ __forceinline__ const float* bias_copy(const AttnOp& a, int h, int di
   return a.vec + ((size_t)(h * 2 + dir) * 4 + s) * a.vec_len;
 }
 
+// Whether the backward takes a sequence and head as one tile of keys and queries.
+bool attn_one_tile(int dt, int seq, int head_dim);
+
 void attn_prep_run(int dt, const AttnOp& a, bool backward, cudaStream_t s);
 void attn_table_grad_run(const AttnOp& a, cudaStream_t s);
 // float32 storage

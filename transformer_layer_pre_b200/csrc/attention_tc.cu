@@ -675,14 +675,16 @@ __device__ __forceinline__ void diagonal_chains(const float (&v)[32], float* out
 // One warp's 32 rows x 64 columns of dS, from its chains into its bins: each of
 // the 95 diagonals is the sum of the chains that cross it; those of one bucket
 // are neighbours and are summed by a segmented scan.  bid: the bucket of
-// diagonal 0 of the block (its column 0, its row 0).
+// diagonal 0 of the block (its column 0, its row 0); DIR: 1 where the columns
+// are keys, -1 where they are queries.
+template <int DIR>
 __device__ __forceinline__ void bin_diagonals(const float* chains, const uint8_t* bid, float* bins, int lane) {
   float s[3];
   int u[3];
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
     const int y = lane + 32 * k;            // diagonal y - 31
-    u[k] = y < 95 ? bid[y - 31] : 256;
+    u[k] = y < 95 ? bid[DIR * (y - 31)] : 256;
     s[k] = 0.0f;
 #pragma unroll
     for (int c = 0; c < kChains; ++c) {
@@ -1116,7 +1118,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[buf]);
-      if (grad && (t.bits & kNear)) bin_diagonals(chains, a.bid + a.vec_off + t.tile * 64 - row0, bins, lane);
+      if (grad && (t.bits & kNear)) bin_diagonals<1>(chains, a.bid + a.vec_off + t.tile * 64 - row0, bins, lane);
     }
     if (grad) flush();
   }
@@ -1124,6 +1126,241 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 13) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------- backward, one tile per sequence and head
+// Sequences up to 128 at head dims up to 64: one block takes a whole (sequence,
+// head), rows = keys, so S and dP are formed once (5 products instead of 7):
+//   S^T = K Q^T, dP^T = V dO^T;  dV = P^T dO, dK = dS^T Q, dQ = dS K
+// D = dO.O is formed here too, from tiles that the products need (dO) or that
+// make room later (O): nothing of size (tokens, hidden) is read twice.
+// Two blocks of 8 warps share an SM, and one block's softmax runs while the
+// other loads, multiplies or writes.  A warp has 32 keys and one half of the
+// queries.
+//
+// TMEM columns: S 0..127, dP 128..255.  P (16-bit) goes to 0..31 (queries
+// 0..63) and 96..127 (the others), which leaves 32..95 for dV; dS goes to
+// shared memory, over the tiles of O and V, where one copy serves as the A
+// operand of dK (its rows) and of dQ (its columns), and dP makes room for
+// dK (128..191) and dQ (192..255).  The results leave through dO, Q and K.
+struct One {
+  static constexpr int kThreads = 256;
+  static constexpr int kWin = 264;                // floats of a window copy: 256 diagonals, 8 banks apart
+  static constexpr int kChainFloats = 8 * kChains * kChain;
+  static constexpr int kSmem = 5 * kRegion + 4 * kWin * 4 + 2 * 128 * 4 + 8 * kAttnMaxBuckets * 4 + kChainFloats * 4 + 48;
+};
+static_assert(2 * (One::kSmem + 1024) <= 228 * 1024, "two blocks do not fit an SM's shared memory");
+
+template <typename T, bool BIAS>
+__global__ void __launch_bounds__(One::kThreads, 2)
+    attention_bwd_one_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                             const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
+                             const __grid_constant__ CUtensorMap tdo, const __grid_constant__ CUtensorMap tdq,
+                             const __grid_constant__ CUtensorMap tdk, const __grid_constant__ CUtensorMap tdv,
+                             const __grid_constant__ AttnOp a) {
+  // the only shared memory of the kernel: its start is 1024-byte aligned
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *sQ = smem_raw, *sK = sQ + kRegion, *sDo = sK + kRegion, *sO = sDo + kRegion, *sV = sO + kRegion;
+  uint8_t* sDs = sO;                                                  // [2] x [128 keys][64 queries]
+  float* sWin = reinterpret_cast<float*>(sV + kRegion);
+  float* vecA = sWin + 4 * One::kWin;                                 // log2(kAttnPUp) - lse2 of every query
+  float* vecB = vecA + 128;                                           // -D / kAttnPUp
+  float* sBins = vecB + 128;
+  float* sChains = sBins + 8 * kAttnMaxBuckets;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sChains + One::kChainFloats);
+  uint64_t *qk_full = bar, *vd_full = bar + 1, *o_full = bar + 2, *s_done = bar + 3, *sums_done = bar + 4;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 5);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int half = warp >> 2, r = (warp & 3) * 32 + lane;             // this thread's queries and key
+  int* err = g_attention_err;
+  if (tid == 0) {
+    for (int i = 0; i < 5; ++i) mbar_init(&bar[i], 1);
+    fence_barrier_init();
+  }
+  if (warp == 0) tmem_alloc(tslot, 256);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  const int bh = blockIdx.x, b = bh / a.nh, h = bh - b * a.nh;
+  const int mb = a.mask_seqs == 1 ? 0 : b;
+  const bool none = a.flags[mb * 2] == 2 && a.flags[mb * 2 + 1] == 2;   // no key left: every gradient is 0
+  const bool grad = BIAS && a.dpart != nullptr;
+  float* bins = sBins + warp * kAttnMaxBuckets;
+  if (grad) {
+    for (int u = lane; u < a.buckets; u += 32) bins[u] = 0.0f;
+    __syncwarp();
+  }
+  bool ok = true;
+  if (!none) {
+    if (tid == 0) {
+      mbar_arrive_expect_tx(qk_full, 2 * kRegion);
+      tma_load_4d(sQ, &tq, qk_full, 0, 0, h, b);
+      tma_load_4d(sK, &tk, qk_full, 0, 0, h, b);
+      mbar_arrive_expect_tx(vd_full, 2 * kRegion);
+      tma_load_4d(sDo, &tdo, vd_full, 0, 0, h, b);
+      tma_load_4d(sV, &tv, vd_full, 0, 0, h, b);
+      mbar_arrive_expect_tx(o_full, kRegion + (BIAS ? 4 * 256 * 4 : 0));
+      tma_load_4d(sO, &to, o_full, 0, 0, h, b);
+      if (BIAS)
+        for (int k = 0; k < 4; ++k)
+          bulk_load_1d(sWin + k * One::kWin, bias_copy(a, h, 1, k) + a.vec_off - 128, 256 * 4, o_full);
+    }
+    const int row = tid >> 1, part = tid & 1;                           // D: two threads to a query
+    const float lse = part && row < a.S ? a.lse[(size_t)bh * a.S + row] : 0.0f;
+    const float mask = a.maskx[(size_t)mb * a.Sp + r];
+    if (tid == 0) {
+      const uint32_t id = idesc_f16(128, 128, std::is_same<T, bf16_t>::value, false, false);
+      const uint64_t dq = desc_k(smem_u32(sQ), 0, kRegion), dk = desc_k(smem_u32(sK), 0, kRegion),
+                     dv = desc_k(smem_u32(sV), 0, kRegion), dd = desc_k(smem_u32(sDo), 0, kRegion);
+      ok = wait_bar<0>(qk_full, 0, err, 401);
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) mma_f16(tmem, dk + kk * 2, dq + kk * 2, id, kk > 0);
+      ok = wait_bar<0>(vd_full, 0, err, 402) && ok;
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) mma_f16(tmem + 128, dv + kk * 2, dd + kk * 2, id, kk > 0);
+      mma_commit(s_done);
+    }
+    __syncwarp();
+    ok = wait_warp<kPauseSoft>(vd_full, 0, err, 403) && ok;
+    ok = wait_warp<kPauseSoft>(o_full, 0, err, 404) && ok;
+    float d = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int at = row * 128 + (((part * 4 + j) ^ (row & 7)) << 4);
+      const uint4 x = *reinterpret_cast<const uint4*>(sO + at), y = *reinterpret_cast<const uint4*>(sDo + at);
+      const T *xe = reinterpret_cast<const T*>(&x), *ye = reinterpret_cast<const T*>(&y);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d = fmaf(to_f(xe[e]), to_f(ye[e]), d);
+    }
+    d += __shfl_xor_sync(0xffffffffu, d, 1);
+    if (part) vecA[row] = row < a.S ? 8.0f - lse * kAttnLog2e : -INFINITY;
+    else vecB[row] = -d * (1.0f / kAttnPUp);
+    __syncthreads();
+    ok = wait_warp<kPauseSoft>(s_done, 0, err, 405) && ok;
+    tc_fence_after();
+
+    // ---- P and dS of this thread's key and 64 queries, 32 at a time; the upper
+    // half goes downwards, so that P lands on columns already read
+    const uint32_t lo = (uint32_t)((warp & 3) * 32) << 16;
+    const int start = 127 - r;   // the row's run of diagonals; copy s is shifted by s + 1
+    const float* wnd = sWin + (start & 3) * One::kWin + (start & ~3) + half * 64;
+    float* chains = sChains + warp * kChains * kChain;
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+      const int c = half ? 1 - k : k, q0 = half * 64 + c * 32;
+      float s[32], dp[32];
+      tmem_ld32_nowait(tmem + lo + q0, s);
+      tmem_ld32_nowait(tmem + lo + 128 + q0, dp);
+      tmem_ld_wait();
+      uint32_t wp[16], wd[16];
+#pragma unroll
+      for (int e = 0; e < 32; e += 4) {
+        const float4 l = *reinterpret_cast<const float4*>(vecA + q0 + e), n = *reinterpret_cast<const float4*>(vecB + q0 + e);
+        float2 add0 = __fadd2_rn(f2(mask), make_float2(l.x, l.y)), add1 = __fadd2_rn(f2(mask), make_float2(l.z, l.w));
+        if (BIAS) {
+          const float4 w = *reinterpret_cast<const float4*>(wnd + c * 32 + e);
+          add0 = __fadd2_rn(add0, make_float2(w.x, w.y));
+          add1 = __fadd2_rn(add1, make_float2(w.z, w.w));
+        }
+        const float2 x0 = __ffma2_rn(make_float2(s[e], s[e + 1]), f2(a.c2), add0);
+        const float2 x1 = __ffma2_rn(make_float2(s[e + 2], s[e + 3]), f2(a.c2), add1);
+        const float2 p0 = make_float2(ex2f(x0.x), ex2f(x0.y)), p1 = make_float2(ex2f(x1.x), ex2f(x1.y));
+        const float2 d0 = __fmul2_rn(p0, __ffma2_rn(make_float2(dp[e], dp[e + 1]), f2(1.0f / kAttnPUp), make_float2(n.x, n.y)));
+        const float2 d1 =
+            __fmul2_rn(p1, __ffma2_rn(make_float2(dp[e + 2], dp[e + 3]), f2(1.0f / kAttnPUp), make_float2(n.z, n.w)));
+        wp[e / 2] = pack2<T>(p0.x, p0.y);
+        wp[e / 2 + 1] = pack2<T>(p1.x, p1.y);
+        wd[e / 2] = pack2<T>(d0.x, d0.y);
+        wd[e / 2 + 1] = pack2<T>(d1.x, d1.y);
+        dp[e] = d0.x, dp[e + 1] = d0.y, dp[e + 2] = d1.x, dp[e + 3] = d1.y;
+      }
+      tmem_st16u(tmem + lo + half * 96 + c * 16, wp);
+      uint8_t* ds = sDs + half * kRegion + r * 128;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4*>(ds + (((c * 4 + j) ^ (r & 7)) << 4)) =
+            make_uint4(wd[4 * j], wd[4 * j + 1], wd[4 * j + 2], wd[4 * j + 3]);
+      if (BIAS && grad) diagonal_chains(dp, chains + 4 * c * kChain, lane);
+    }
+    tmem_store_wait();
+    tc_fence_before();
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (tid == 0) {
+      constexpr bool bf = std::is_same<T, bf16_t>::value;
+      const uint32_t id = idesc_f16(128, 64, bf, false, true), id_q = idesc_f16(128, 64, bf, true, true);
+      const uint64_t dq = desc_mn(smem_u32(sQ), 0, kRegion), dk = desc_mn(smem_u32(sK), 0, kRegion),
+                     dd = desc_mn(smem_u32(sDo), 0, kRegion);
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        mma_f16_ts(tmem + 32, tmem + (kk >> 2) * 96 + (kk & 3) * 8, dd + kk * 128, id, kk > 0);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        mma_f16(tmem + 128, desc_k(smem_u32(sDs), kk, kRegion), dq + kk * 128, id, kk > 0);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        mma_f16(tmem + 192, desc_mn(smem_u32(sDs), kk, kRegion), dk + kk * 128, id_q, kk > 0);
+      mma_commit(sums_done);
+    }
+    __syncwarp();
+    if (grad) bin_diagonals<-1>(chains, a.bid + a.vec_off - half * 64 + (warp & 3) * 32, bins, lane);
+  }
+  if (grad) {
+    __syncthreads();
+    for (int u = tid; u < a.buckets; u += One::kThreads) {
+      float t = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) t += sBins[w * kAttnMaxBuckets + u];
+      a.dpart[(size_t)bh * a.buckets + u] = t;
+    }
+  }
+  if (!none) {
+    ok = wait_warp<kPauseSoft>(sums_done, 0, err, 406) && ok;
+    tc_fence_after();
+  }
+  // ---- dV by the lower warps, dK by the upper ones, half of dQ each
+#pragma unroll 1
+  for (int k = 0; k < 3; ++k) {
+    const uint32_t col = k == 2 ? 192 + half * 32 : (half ? 128 : 32) + k * 32;
+    uint8_t* out = k == 2 ? sK : (half ? sQ : sDo);
+    const int c = k == 2 ? half : k;
+    const float f = k == 2 || half ? a.scale : 1.0f / kAttnPUp;
+    float v[32];
+    tmem_ld32_nowait(tmem + ((uint32_t)((warp & 3) * 32) << 16) + col, v);
+    tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = none ? 0u : pack2<T>(v[e * 8 + 2 * j] * f, v[e * 8 + 2 * j + 1] * f);
+      *reinterpret_cast<uint4*>(out + r * 128 + (((c * 4 + e) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  tc_fence_before();
+  fence_proxy_async_smem();
+  __syncthreads();
+  if (tid == 0) {
+    if (ok) {
+      tma_store_4d(&tdv, sDo, 0, 0, h, b);
+      tma_store_4d(&tdk, sQ, 0, 0, h, b);
+      tma_store_4d(&tdq, sK, 0, 0, h, b);
+      bulk_commit();
+      bulk_wait_all();
+    } else {
+      // a wait gave up: what was issued lands before the block exits
+      for (int i = 0; i < 3; ++i) mbar_wait(&bar[i], 0, nullptr, 0);
+    }
+  }
+  __syncwarp();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, 256);
 }
 
 // ------------------------------------------------------------------ host side
@@ -1189,6 +1426,21 @@ bool bwd(const AttnOp& a, cudaStream_t s) {
   return true;
 }
 
+template <typename T, bool BIAS>
+bool bwd_one(const AttnOp& a, cudaStream_t s) {
+  const bool bf = std::is_same<T, bf16_t>::value;
+  CUtensorMap mq, mk, mv, mo, mdo, mdq, mdk, mdv;
+  if (!encode(&mq, a.q, a, bf, 128) || !encode(&mk, a.k, a, bf, 128) || !encode(&mv, a.v, a, bf, 128) ||
+      !encode(&mo, a.o, a, bf, 128) || !encode(&mdo, a.dout, a, bf, 128) || !encode(&mdq, a.dq, a, bf, 128) ||
+      !encode(&mdk, a.dk, a, bf, 128) || !encode(&mdv, a.dv, a, bf, 128))
+    return false;
+  static std::atomic<uint64_t> ready{0};
+  allow_smem(attention_bwd_one_kernel<T, BIAS>, One::kSmem, ready);
+  launch_pdl(attention_bwd_one_kernel<T, BIAS>, a.B * a.nh, One::kThreads, One::kSmem, s, mq, mk, mv, mo, mdo, mdq, mdk, mdv, a);
+  count_launch();
+  return true;
+}
+
 }  // namespace
 
 bool attention_tc_fwd_run(int dt, const AttnOp& a, cudaStream_t s) {
@@ -1198,6 +1450,10 @@ bool attention_tc_fwd_run(int dt, const AttnOp& a, cudaStream_t s) {
 
 bool attention_tc_bwd_run(int dt, const AttnOp& a, cudaStream_t s) {
   const bool h = dt == DT_F16;
+  if (attn_one_tile(dt, a.S, a.d)) {
+    if (a.vec) return h ? bwd_one<half_t, true>(a, s) : bwd_one<bf16_t, true>(a, s);
+    return h ? bwd_one<half_t, false>(a, s) : bwd_one<bf16_t, false>(a, s);
+  }
   if (a.S > kLongSeq) {
     if (a.d <= 64) return h ? bwd<half_t, 64, true>(a, s) : bwd<bf16_t, 64, true>(a, s);
     return h ? bwd<half_t, 128, true>(a, s) : bwd<bf16_t, 128, true>(a, s);
