@@ -273,3 +273,35 @@ def test_small_probabilities_of_a_long_row(dtype):
     assert float((lse.double() - math.log(s)).abs().max()) <= 2.0 ** -18
     assert float((dv.double() - 1).abs().max()) <= 2 * u + s / 16 * 2.0 ** -23 + 2.0 ** -18
     assert bool((dk == 0).all()) and bool(torch.isfinite(dq).all())
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("buckets", [0, 32])
+@pytest.mark.parametrize("mask", ["none", "lowest", "holes"])
+def test_many_short_sequences(dtype, buckets, mask):
+    """More (sequence, head) pairs than blocks at a time, ones without a key first and, in the other mask, none."""
+    _case(dtype, 120, 100, 7, 48, mask=mask, buckets=buckets)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_short_sequences_without_a_key_among_others(dtype):
+    """A block's items go on between ones with and without a key, in every order: gradients of the former as when they
+    are alone, of the latter 0."""
+    b, s, n, d = 96, 33, 16, 64
+    g = torch.Generator(device="cuda").manual_seed(11)
+    q, k, v, do = (torch.randn(b, s, n, d, generator=g, device="cuda").to(DT[dtype]) for _ in range(4))
+    table = torch.randn(32, n, generator=g, device="cuda").to(DT[dtype])
+    m = torch.zeros(b, s, device="cuda")
+    gone = torch.rand(b, generator=g, device="cuda") < 0.5
+    m[gone] = -math.inf
+    o, lse = tlp.attention_forward(q, k, v, m, table)
+    got = tlp.attention_backward(q, k, v, o, lse, do, m, table)
+    live = ~gone
+    part = [t[live].contiguous() for t in (q, k, v, do)]
+    o2, lse2 = tlp.attention_forward(*part[:3], None, table)
+    want = tlp.attention_backward(*part[:3], o2, lse2, part[3], None, table)
+    tlp.device_check()
+    assert torch.equal(o[live], o2) and bool((o[gone] == 0).all())
+    for x, y in zip(got[:3], want[:3]):
+        assert torch.equal(x[live], y) and bool((x[gone] == 0).all())
+    assert torch.equal(got[3], want[3])      # the same partial sums, and zeros, in float64

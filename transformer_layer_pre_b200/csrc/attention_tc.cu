@@ -1191,10 +1191,12 @@ __global__ void __launch_bounds__(One::kThreads, 2)
   const bool none = a.flags[mb * 2] == 2 && a.flags[mb * 2 + 1] == 2;   // no key left: every gradient is 0
   const bool grad = BIAS && a.dpart != nullptr;
   float* bins = sBins + warp * kAttnMaxBuckets;
+  float* chains = sChains + warp * kChains * kChain;
   if (grad) {
     for (int u = lane; u < a.buckets; u += 32) bins[u] = 0.0f;
     __syncwarp();
   }
+  auto bin = [&] { bin_diagonals<-1>(chains, a.bid + a.vec_off - half * 64 + (warp & 3) * 32, bins, lane); };
   bool ok = true;
   if (!none) {
     if (tid == 0) {
@@ -1250,7 +1252,6 @@ __global__ void __launch_bounds__(One::kThreads, 2)
     const uint32_t lo = (uint32_t)((warp & 3) * 32) << 16;
     const int start = 127 - r;   // the row's run of diagonals; copy s is shifted by s + 1
     const float* wnd = sWin + (start & 3) * One::kWin + (start & ~3) + half * 64;
-    float* chains = sChains + warp * kChains * kChain;
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
       const int c = half ? 1 - k : k, q0 = half * 64 + c * 32;
@@ -1310,18 +1311,8 @@ __global__ void __launch_bounds__(One::kThreads, 2)
       mma_commit(sums_done);
     }
     __syncwarp();
-    if (grad) bin_diagonals<-1>(chains, a.bid + a.vec_off - half * 64 + (warp & 3) * 32, bins, lane);
-  }
-  if (grad) {
-    __syncthreads();
-    for (int u = tid; u < a.buckets; u += One::kThreads) {
-      float t = 0.0f;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) t += sBins[w * kAttnMaxBuckets + u];
-      a.dpart[(size_t)bh * a.buckets + u] = t;
-    }
-  }
-  if (!none) {
+    // warp 0, whose thread issues the products, does so behind the stores
+    if (grad && warp > 0) bin();
     ok = wait_warp<kPauseSoft>(sums_done, 0, err, 406) && ok;
     tc_fence_after();
   }
@@ -1346,21 +1337,30 @@ __global__ void __launch_bounds__(One::kThreads, 2)
   tc_fence_before();
   fence_proxy_async_smem();
   __syncthreads();
-  if (tid == 0) {
-    if (ok) {
-      tma_store_4d(&tdv, sDo, 0, 0, h, b);
-      tma_store_4d(&tdk, sQ, 0, 0, h, b);
-      tma_store_4d(&tdq, sK, 0, 0, h, b);
-      bulk_commit();
-      bulk_wait_all();
-    } else {
-      // a wait gave up: what was issued lands before the block exits
-      for (int i = 0; i < 3; ++i) mbar_wait(&bar[i], 0, nullptr, 0);
-    }
+  if (tid == 0 && ok) {
+    tma_store_4d(&tdv, sDo, 0, 0, h, b);
+    tma_store_4d(&tdk, sQ, 0, 0, h, b);
+    tma_store_4d(&tdq, sK, 0, 0, h, b);
+    bulk_commit();
   }
   __syncwarp();
   tc_fence_after();
   if (warp == 0) tmem_dealloc(tmem, 256);
+  if (grad) {
+    if (warp == 0 && !none) bin();
+    __syncthreads();
+    for (int u = tid; u < a.buckets; u += One::kThreads) {
+      float t = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) t += sBins[w * kAttnMaxBuckets + u];
+      a.dpart[(size_t)bh * a.buckets + u] = t;
+    }
+  }
+  if (tid == 0) {
+    bulk_wait_all();
+    // a wait gave up: what was issued lands before the block exits
+    for (int i = 0; i < 3 && !ok; ++i) mbar_wait(&bar[i], 0, nullptr, 0);
+  }
 }
 
 // ------------------------------------------------------------------ host side
