@@ -24,7 +24,9 @@ constexpr int kPrepRows = 4;        // rows of O and dO in flight per group of l
 // of 4 * 256 / G rows for stats, G lanes per row reading 16 bytes each; rows run
 // (b, token, head) with the head fastest, the order in which O and dO lie in
 // (B, S, heads, d) memory.
-// Bound: HBM in the backward (reads O and dO once), launch latency otherwise.
+// Bound: launch latency (5 us) in the forward and where the backward forms D
+// itself; else HBM: O and dO of B16 h16 d64 S512, 33.6 MB, 14 us.  Rows dealt with
+// the token fastest took 15 us, two rows in flight 16.
 template <typename T, int G>
 __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(const __grid_constant__ AttnOp a, int nmask, int nvec, int nzero) {
   pdl_wait();
@@ -123,7 +125,8 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(const __grid_co
 
 // dtable[u, h] (+)= sum over sequences and items of dpart, in a fixed order
 // and in float64: a block per head and 32 buckets, a lane per bucket (whole
-// lines of dpart), the rows dealt to the warps.
+// lines of dpart), the rows dealt to the warps.  Bound: latency; 3.5 us for 64 rows
+// per head of 16 heads and 32 buckets, 5.8 for 512.
 constexpr int kTableWarps = 32;
 __global__ void __launch_bounds__(32 * kTableWarps) attn_table_grad_kernel(const __grid_constant__ AttnOp a) {
   __shared__ double red[kTableWarps][33];

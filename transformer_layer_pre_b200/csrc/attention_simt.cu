@@ -12,6 +12,10 @@
 //   key rows    S^T = K Q^T, dP^T = V dO^T;  dV += P^T dO, dK += dS^T Q
 //   query rows  S   = Q K^T, dP   = dO V^T;  dQ += dS K, and the bias
 //               gradient: dS summed along its diagonals, then by bucket.
+//
+// Bound: FP32 FMAs and the shared-memory reads that feed them (two float4 per 16
+// FMAs), and too few blocks for the SMs at small batches: 6 to 12 TFLOP/s; B1 h4
+// d64 S1024 forward 103 us with 64 blocks on 148 SMs.
 #include <math.h>
 
 #include "attention.cuh"

@@ -202,6 +202,14 @@ struct LiveTiles {
 // tile's 255 diagonals are staged as four copies shifted by one float each, so
 // that every row reads its run of 128 in aligned float4 without bank
 // conflicts.
+//
+// Bound: the special-function unit (16 exponentials per clock and SM against
+// 128 x 64 of them per tile) and the latency of a tile's chain product -> maximum
+// -> exponentials -> product.  B4 h16 d64 S2048: 140 us, 490 TFLOP/s (0.30 of the
+// measured GEMM rate), exponentials 52 % of their unit's rate, tensor pipe 26 %;
+// h8 d128: 97 us, 706 TFLOP/s; B64 h16 S128, 67.6 MB: 21 us, 3.2 TB/s.
+// Per 128 x 64 tile: two blocks of 128-key tiles on an SM took 168 us, four of 64
+// keys 146; windows read straight from global memory 159.
 template <int D>
 struct Fwd {
   static constexpr int kTK = D == 64 ? 64 : 128;                    // keys per tile
@@ -615,8 +623,14 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
 // subnormals, whose rounding is absolute, up to S = 2^22.  The factor comes with
 // -lse2, leaves dS through the product dP / kAttnPUp - D / kAttnPUp, and dV as it
 // is written out; all of it is exact.
-// TMEM: per softmax group S, dP (64 columns each); from 256 on the sums, two
-// sets of them for D = 64, so the next item starts while one is written out.
+// TMEM: two or three buffers of S and dP (64 columns each), then the sums: one
+// set of two, or two sets, so that the next item starts while one is written out.
+//
+// Bound: the chain of a tile (operands, product, exponentials, product) through
+// the barriers between its warps: tensor pipe 33 %, exponentials 38 %, issue
+// slots 40 % busy.  B4 h16 d64 S2048: 363 us, 473 TFLOP/s of the 5 products that
+// the formulas have (662 of the 7 formed); h8 d128: 291 us, 590 TFLOP/s; B16 h16
+// S512 padded: 150 us.
 constexpr int kRun = 192, kWin = 200;           // diagonals of a 128 x 64 tile, floats of a window copy
 constexpr int kVecs = 4 * kWin * 4;             // column vectors after the four copies
 constexpr int kChain = 40;                      // floats of a diagonal chain
@@ -1136,7 +1150,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // make room later (O): nothing of size (tokens, hidden) is read twice.
 // Two blocks of 8 warps share an SM, and one block's softmax runs while the
 // other loads, multiplies or writes.  A warp has 32 keys and one half of the
-// queries.
+// queries.  Head dim 128 would leave room for one block only and takes the
+// kernel above.
+//
+// Bound: HBM (five tiles in, three out; rows of 128 bytes) behind the latency of
+// a pair's load, two rounds of products and write: B64 h16 S128, 134.7 MB, 41 us,
+// 3.2 TB/s; loads and stores alone 26 us.  The kernel above took 57 us there, and
+// 14 more for D in the prepared workspace.  One block walking several pairs (the
+// next V and O loaded ahead, prefetched to L2, or dQ written straight to its rows
+// so that Q, K and dO load ahead too) came to the same or 2 us more.
 //
 // TMEM columns: S 0..127, dP 128..255.  P (16-bit) goes to 0..31 (queries
 // 0..63) and 96..127 (the others), which leaves 32..95 for dV; dS goes to
