@@ -305,3 +305,67 @@ def test_short_sequences_without_a_key_among_others(dtype):
     for x, y in zip(got[:3], want[:3]):
         assert torch.equal(x[live], y) and bool((x[gone] == 0).all())
     assert torch.equal(got[3], want[3])      # the same partial sums, and zeros, in float64
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("mask", ["none", "lengths", "holes", "lowest", "values", "late", "empty"])
+@pytest.mark.parametrize("buckets", [0, 32])
+def test_short_masks(dtype, mask, buckets):
+    _case(dtype, 3, 128, 2, 64, mask=mask, buckets=buckets)
+    _case(dtype, 2, 90, 3, 40, mask=mask, buckets=buckets)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("buckets,distance", [(4, 2), (4, 1000), (8, 3), (16, 64), (32, 33), (128, 1024), (256, 65)])
+def test_short_buckets(dtype, buckets, distance):
+    _case(dtype, 2, 121, 2, 64, buckets=buckets, distance=distance, spread=3.0)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("layout", ["packed", "bhsd", "padded"])
+@pytest.mark.parametrize("d", [8, 24, 56, 64])
+def test_short_layouts(dtype, layout, d):
+    _case(dtype, 3, 65, 3, d, layout=layout, mask="lengths")
+    _case(dtype, 1, 1, 1, d, layout=layout)
+
+
+def test_short_and_long_calls_at_once_and_in_graphs():
+    """Kernels that take all of an SM's tensor memory and ones that take half of it, on two streams, then in two graphs
+    that replay side by side."""
+    g = torch.Generator(device="cuda").manual_seed(12)
+    sets = []
+    for b, s, n in ((40, 100, 8), (2, 700, 8)):
+        q, k, v, do = (torch.randn(b, s, n, 64, generator=g, device="cuda").bfloat16() for _ in range(4))
+        sets.append((q, k, v, do, torch.randn(32, n, generator=g, device="cuda").bfloat16(), _mask("lengths", b, s, g)))
+
+    def step(q, k, v, do, table, mask):
+        o, lse = tlp.attention_forward(q, k, v, mask=mask, bias_table=table)
+        return (o, lse) + tlp.attention_backward(q, k, v, o, lse, do, mask=mask, bias_table=table)
+
+    want = [step(*x) for x in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        got = [None, None]
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                for _ in range(4):
+                    got[i] = step(*sets[i])
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for w, r in zip(want, got) for x, y in zip(w, r))
+    graphs, outs = [], []
+    for x in sets:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(step(*x))
+    for _ in range(5):
+        for o in outs:
+            for t in o:
+                t.zero_()
+        torch.cuda.synchronize()
+        for st, gr in zip(streams, graphs):
+            with torch.cuda.stream(st):
+                gr.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for w, r in zip(want, outs) for x, y in zip(w, r))
+    tlp.device_check()

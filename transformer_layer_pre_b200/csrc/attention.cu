@@ -61,8 +61,15 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(const __grid_co
     const int h = blk / per, X = (blk - h * per) * kPrepThreads + tid;
     if (X >= a.vec_len) return;
     const int x = max(-a.sat, min(a.sat, X - a.vec_off));   // key minus query
+    // the last bucket of the side that begins at or before the distance
+    const int half = a.buckets / 2, dist = abs(x);
     int u = 0;
-    while (u < a.buckets - 1 && !(x >= a.lo[u] && x - a.lo[u] < a.n[u])) ++u;
+    for (int end = half - 1; u < end;) {
+      const int mid = (u + end + 1) >> 1;
+      if (a.lo[half + mid] <= dist) u = mid;
+      else end = mid - 1;
+    }
+    if (x > 0) u += half;
     const float v = to_f(static_cast<const T*>(a.table)[(size_t)u * a.nh + h]) * kAttnLog2e;
     if (h == 0) a.bid[X] = (uint8_t)u;
 #pragma unroll
