@@ -24,7 +24,7 @@ constexpr int kPrepRows = 4;        // rows of O and dO in flight per group of l
 // of 4 * 256 / G rows for stats, G lanes per row reading 16 bytes each; rows run
 // (b, token, head) with the head fastest, the order in which O and dO lie in
 // (B, S, heads, d) memory.
-// Bound: launch latency (5 us) in the forward and where the backward forms D
+// Bound: launch latency (3 us) in the forward and where the backward forms D
 // itself; else HBM: O and dO of B16 h16 d64 S512, 33.6 MB, 14 us.  Rows dealt with
 // the token fastest took 15 us, two rows in flight 16.
 template <typename T, int G>

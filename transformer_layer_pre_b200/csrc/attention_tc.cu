@@ -205,9 +205,9 @@ struct LiveTiles {
 //
 // Bound: the special-function unit (16 exponentials per clock and SM against
 // 128 x 64 of them per tile) and the latency of a tile's chain product -> maximum
-// -> exponentials -> product.  B4 h16 d64 S2048: 140 us, 490 TFLOP/s (0.30 of the
+// -> exponentials -> product.  B4 h16 d64 S2048: 138 us, 498 TFLOP/s (0.30 of the
 // measured GEMM rate), exponentials 52 % of their unit's rate, tensor pipe 26 %;
-// h8 d128: 97 us, 706 TFLOP/s; B64 h16 S128, 67.6 MB: 21 us, 3.2 TB/s.
+// h8 d128: 95 us, 721 TFLOP/s; B64 h16 S128, 67.6 MB: 21 us, 3.2 TB/s.
 // Per 128 x 64 tile: two blocks of 128-key tiles on an SM took 168 us, four of 64
 // keys 146; windows read straight from global memory 159.
 template <int D>
@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
 // Bound: the chain of a tile (operands, product, exponentials, product) through
 // the barriers between its warps: tensor pipe 33 %, exponentials 38 %, issue
 // slots 40 % busy.  B4 h16 d64 S2048: 363 us, 473 TFLOP/s of the 5 products that
-// the formulas have (662 of the 7 formed); h8 d128: 291 us, 590 TFLOP/s; B16 h16
+// the formulas have (662 of the 7 formed); h8 d128: 290 us, 593 TFLOP/s; B16 h16
 // S512 padded: 150 us.
 constexpr int kRun = 192, kWin = 200;           // diagonals of a 128 x 64 tile, floats of a window copy
 constexpr int kVecs = 4 * kWin * 4;             // column vectors after the four copies
