@@ -643,12 +643,19 @@ struct Bwd {
   static constexpr int kSlots = D == 128 && LONG ? 1 : 2;           // stationary pairs
   static constexpr int kNs = D == 64 || LONG ? 4 : 2;               // moving pairs
   static constexpr int kBuf = D == 64 && LONG ? 3 : 2;              // S, dP buffers
+  // Barriers of finished scores.  Two groups take the tiles in turn, and a wait
+  // for a parity cannot tell the phase before the last one done from its own: a
+  // barrier belongs to one group, which then waits for each of its phases.
+  static constexpr int kFull = kBuf % 2 ? 2 * kBuf : kBuf;
   static constexpr int kAcc = D == 64 && !LONG ? 2 : 1;             // sets of sums
   static constexpr uint32_t kSums = kBuf * 128;                     // their first TMEM column
   static constexpr int kAuxBytes = kVecs + 512 + 16;                // window, two column vectors, description
   static constexpr int kStAux = 2 * 128 * 4 + 16;                   // row vectors, empty flag
   static constexpr int kSmem = kSlots * 2 * kSt + 2 * kNs * kMv + kNs * kAuxBytes + kSlots * kStAux +
                                8 * kAttnMaxBuckets * 4 + 8 * kChains * kChain * 4 + 400;
+  static constexpr int kBars = 2 * kSlots + 2 * kNs + kFull + 2 * kBuf + 2 * kAcc;
+  static_assert(kFull % 2 == 0, "a barrier of finished scores serves both softmax groups");
+  static_assert(kBars * 8 + 4 <= 400, "the barriers do not fit their shared memory");
   static_assert(kSums + kAcc * 2 * D <= 512, "the sums do not fit the tensor memory");
   static_assert(kSmem <= 227 * 1024, "the backward's shared memory exceeds a block's maximum");
 };
@@ -804,7 +811,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   float* sChains = sBins + 8 * kAttnMaxBuckets;
   uint64_t* bar = reinterpret_cast<uint64_t*>(sChains + 8 * kChains * kChain);
   uint64_t *st_full = bar, *st_empty = st_full + C::kSlots, *mv_full = st_empty + C::kSlots,
-           *mv_empty = mv_full + C::kNs, *s_full = mv_empty + C::kNs, *p_full = s_full + C::kBuf, *s_free = p_full + C::kBuf,
+           *mv_empty = mv_full + C::kNs, *s_full = mv_empty + C::kNs, *p_full = s_full + C::kFull, *s_free = p_full + C::kBuf,
            *acc_full = s_free + C::kBuf, *acc_free = acc_full + C::kAcc;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(acc_free + C::kAcc);
 
@@ -812,7 +819,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   int* err = g_attention_err;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kSlots; ++i) mbar_init(&st_full[i], 1), mbar_init(&st_empty[i], 1);
-    for (int i = 0; i < C::kBuf; ++i) mbar_init(&s_full[i], 2), mbar_init(&p_full[i], 4), mbar_init(&s_free[i], 1);
+    for (int i = 0; i < C::kFull; ++i) mbar_init(&s_full[i], 2);
+    for (int i = 0; i < C::kBuf; ++i) mbar_init(&p_full[i], 4), mbar_init(&s_free[i], 1);
     for (int i = 0; i < C::kNs; ++i) mbar_init(&mv_full[i], 1), mbar_init(&mv_empty[i], 1);
     for (int i = 0; i < C::kAcc; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_free[i], 4);
     fence_barrier_init();
@@ -931,6 +939,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const uint64_t dst = desc_k(smem_u32(sSt), 0, kRegion), dmv = desc_k(smem_u32(sMv), 0, C::kMvRegion);
       for (uint32_t g = 0, ends = 0; ends < 2; ++g) {
         const int ms = g % C::kNs, w = g % C::kBuf;
+        uint64_t* sf = &s_full[g % C::kFull];
         if (!wait_bar<0>(&mv_full[ms], (g / C::kNs) & 1, err, 313)) break;
         const TileInfo t = *info_of(g);
         const int slot = t.item % C::kSlots;
@@ -939,8 +948,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (!wait_bar<0>(&s_free[w], ((g / C::kBuf) & 1) ^ 1, err, 316)) break;
         if (t.tile < 0) {
           if (t.bits & kEnd) ++ends;
-          mbar_arrive(&s_full[w]);
-          mbar_arrive(&s_full[w]);
+          mbar_arrive(sf);
+          mbar_arrive(sf);
           continue;
         }
         tc_fence_after();
@@ -955,8 +964,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int kk = 0; kk < D / 16; ++kk)
           mma_f16(tS + 64, a2 + (kk >> 2) * (kRegion >> 4) + (kk & 3) * 2,
                   b2 + (kk >> 2) * (C::kMvRegion >> 4) + (kk & 3) * 2, id, kk > 0);
-        mma_commit(&s_full[w]);
-        mbar_arrive(&s_full[w]);   // orders what this thread waited for; the commit, the products
+        mma_commit(sf);
+        mbar_arrive(sf);   // orders what this thread waited for; the commit, the products
       }
     }
   } else if (warp == 14) {
@@ -1085,7 +1094,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // S is there, and with it everything that its issuing thread waited for:
       // the description, the vectors, the item's row vectors (each wait costs
       // 150 clocks even when there is nothing to wait for)
-      if (!wait_warp<kPauseSoft>(&s_full[buf], (g / C::kBuf) & 1, err, 333)) break;
+      if (!wait_warp<kPauseSoft>(&s_full[g % C::kFull], (g / C::kFull) & 1, err, 333)) break;
       const TileInfo t = *info_of(g);
       if (t.bits & kEnd) {
         if (lane == 0) mbar_arrive(&p_full[buf]);
