@@ -555,39 +555,40 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full);
       }
-      if (!ok) break;
       // ---- the item's rows: O / l through the Q tile (no product reads it any more)
-      if (!(ok = wait_warp<0>(pv_done, n & 1, err, 225))) break;
-      tc_fence_after();
-      uint8_t* stage = sQ;
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      if (ok && (ok = wait_warp<0>(pv_done, n & 1, err, 225))) {
+        tc_fence_after();
+        uint8_t* stage = sQ;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        float o[32];
-        tmem_ld32_nowait(tmem + lo + C::kO + c * 32, o);
-        tmem_ld_wait();
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
+          tmem_ld32_nowait(tmem + lo + C::kO + c * 32, o);
+          tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t w[4];
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            // an empty row may never have had a product
-            const float y0 = l == 0.0f ? 0.0f : o[e * 8 + 2 * k] * inv;
-            const float y1 = l == 0.0f ? 0.0f : o[e * 8 + 2 * k + 1] * inv;
-            w[k] = pack2<T>(y0, y1);
+            for (int k = 0; k < 4; ++k) {
+              // an empty row may never have had a product
+              const float y0 = l == 0.0f ? 0.0f : o[e * 8 + 2 * k] * inv;
+              const float y1 = l == 0.0f ? 0.0f : o[e * 8 + 2 * k + 1] * inv;
+              w[k] = pack2<T>(y0, y1);
+            }
+            const int ch = c * 4 + e;   // 16-byte chunk of the row
+            *reinterpret_cast<uint4*>(stage + (ch >> 3) * kRegion + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
           }
-          const int ch = c * 4 + e;   // 16-byte chunk of the row
-          *reinterpret_cast<uint4*>(stage + (ch >> 3) * kRegion + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
         }
+        tc_fence_before();
+        const int row = i * 128 + r;
+        if (row < a.S) a.lse[(size_t)bh * a.S + row] = l == 0.0f ? INFINITY : (ref + log2f(l)) * kAttnLn2;
+        fence_proxy_async_smem();
       }
-      tc_fence_before();
-      const int row = i * 128 + r;
-      if (row < a.S) a.lse[(size_t)bh * a.S + row] = l == 0.0f ? INFINITY : (ref + log2f(l)) * kAttnLn2;
-      fence_proxy_async_smem();
-      named_barrier(1, 128);
+      // each warp times its own waits: all four go on, or none does
+      if (!(ok = named_barrier_all(1, 128, ok))) break;
       if (threadIdx.x == 0) {
-        for (int c = 0; c < D / 64; ++c) tma_store_4d(&to, stage + c * kRegion, c * 64, i * 128, h, b);
+        for (int c = 0; c < D / 64; ++c) tma_store_4d(&to, sQ + c * kRegion, c * 64, i * 128, h, b);
         bulk_commit();
         bulk_wait_read<0>();
         mbar_arrive(q_empty);
@@ -1012,37 +1013,39 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const bool keys = it < items;
       const int x = keys ? it : it - items, bh = x / nr, ri = x - bh * nr, b = bh / a.nh, h = bh - b * a.nh;
       const int slot = n % C::kSlots, ab = n % C::kAcc;
-      if (!(ok = wait_warp<kPauseStore>(&st_full[slot], (n / C::kSlots) & 1, err, 321))) break;
-      const bool none = *none_flag(n) != 0;
-      if (!(ok = wait_warp<kPauseStore>(&acc_full[ab], (n / C::kAcc) & 1, err, 322))) break;
-      tc_fence_after();
       uint8_t* st = sSt + slot * 2 * C::kSt;
+      ok = wait_warp<kPauseStore>(&st_full[slot], (n / C::kSlots) & 1, err, 321);
+      const bool none = ok && *none_flag(n) != 0;
+      if (ok && (ok = wait_warp<kPauseStore>(&acc_full[ab], (n / C::kAcc) & 1, err, 322))) {
+        tc_fence_after();
 #pragma unroll 1
-      for (int q = 0; q < (keys ? 2 : 1); ++q) {
-        const float f = q == 0 ? a.scale : 1.0f / kAttnPUp;
-        uint8_t* out = st + q * C::kSt;
+        for (int q = 0; q < (keys ? 2 : 1); ++q) {
+          const float f = q == 0 ? a.scale : 1.0f / kAttnPUp;
+          uint8_t* out = st + q * C::kSt;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          float v[32];
-          tmem_ld32_nowait(tmem + lo + C::kSums + ab * 2 * D + q * D + c * 32, v);
-          tmem_ld_wait();
+          for (int c = 0; c < D / 32; ++c) {
+            float v[32];
+            tmem_ld32_nowait(tmem + lo + C::kSums + ab * 2 * D + q * D + c * 32, v);
+            tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t w[4];
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = none ? 0u : pack2<T>(v[e * 8 + 2 * k] * f, v[e * 8 + 2 * k + 1] * f);
-            const int ch = c * 4 + e;
-            *reinterpret_cast<uint4*>(out + (ch >> 3) * kRegion + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
+              for (int k = 0; k < 4; ++k)
+                w[k] = none ? 0u : pack2<T>(v[e * 8 + 2 * k] * f, v[e * 8 + 2 * k + 1] * f);
+              const int ch = c * 4 + e;
+              *reinterpret_cast<uint4*>(out + (ch >> 3) * kRegion + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_free[ab]);
+        fence_proxy_async_smem();
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_free[ab]);
-      fence_proxy_async_smem();
-      named_barrier(1, 128);
+      // each warp times its own waits: all four go on, or none does
+      if (!(ok = named_barrier_all(1, 128, ok))) break;
       if (r == 0) {
         for (int c = 0; c < D / 64; ++c) {
           tma_store_4d(keys ? &tdk : &tdq, st + c * kRegion, c * 64, ri * 128, h, b);
