@@ -286,7 +286,10 @@ tl_status tl_bias_grad_noalloc(int dtype, const void* dz, int rows, int cols, fl
  *   dT[u, h] = sum of dS_ij over every sequence and every i, j with bucket(j - i) = u
  * No dropout.  Scores, softmax and sums are float32; 16-bit storage rounds P
  * and dS to the storage type for their products (tensor cores), float32
- * storage rounds nothing.  Results are bitwise reproducible.
+ * storage rounds nothing.  float16 holds dS at a power of two chosen per
+ * sequence and head from the largest |dO| and |V| (removed keys and empty rows
+ * left out), so small and large gradients keep its precision.  Results are
+ * bitwise reproducible.
  *
  * Buckets: half of them for keys at or behind the query (bucket(x) = f(-x) for
  * x <= 0), half for keys ahead (bucket(x) = buckets/2 + f(x)); with h =

@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/tlp.h"
 #include "attention.cuh"
@@ -14,19 +15,13 @@
 namespace tlp {
 namespace {
 
-constexpr int kPrepThreads = 256;
-constexpr int kPrepRows = 4;        // rows of O and dO in flight per group of lanes
-
 // One launch fills the workspace (layout at the top of attention.cuh).
 // Blocks [0, nmask): 256 keys each of maskx and flags.  Then nvec blocks: 256
 // diagonals of one head each, written to every copy.  Then (backward) nzero
-// blocks that clear dpart, and blocks
-// of 4 * 256 / G rows for stats, G lanes per row reading 16 bytes each; rows run
-// (b, token, head) with the head fastest, the order in which O and dO lie in
-// (B, S, heads, d) memory.
-// Bound: launch latency (3 us) in the forward and where the backward forms D
-// itself; else HBM: O and dO of B16 h16 d64 S512, 33.6 MB, 14 us.  Rows dealt with
-// the token fastest took 15 us, two rows in flight 16.
+// blocks that clear dpart, and blocks of prep_rows(G) * 256 / G tokens of one
+// sequence and head for stats (and, float16, smax), G lanes per row reading 16
+// bytes each.
+// Bound: launch latency (3 us) in the forward and where the backward forms D itself.
 template <typename T, int G>
 __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(const __grid_constant__ AttnOp a, int nmask, int nvec, int nzero) {
   pdl_wait();
@@ -89,43 +84,67 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(const __grid_co
     return;
   }
   blk -= nzero;
-  constexpr int kEl = 16 / sizeof(T);
+  constexpr bool kMax = std::is_same<T, half_t>::value;
+  constexpr int kEl = 16 / sizeof(T), kRows = prep_rows(G), kStep = kPrepThreads / G;
   const int lane = tid % G;
-  const unsigned rows = (unsigned)a.B * a.Sp * a.nh;    // at most 2^30
-  unsigned row[kPrepRows];
-  float t[kPrepRows];
-  size_t at[kPrepRows];                                 // of the row's stats
-  int tok[kPrepRows];
+  // neighbouring blocks take the heads of the same tokens, which lie side by side in (B, S, heads, d) memory
+  const int per = a.Sp / (kRows * kStep), bc = blk / a.nh, h = blk - bc * a.nh, b = bc / per, chunk = bc - b * per;
+  const int bh = b * a.nh + h;
+  const int i0 = chunk * kRows * kStep + tid / G;
+  float t[kRows];                                       // dO.O
+  __half2 mdo[kRows], mv[kRows];                        // largest |dO| and |V|, of even and odd dims
 #pragma unroll
-  for (int k = 0; k < kPrepRows; ++k) {
-    row[k] = ((unsigned)blk * kPrepRows + k) * (kPrepThreads / G) + tid / G;
-    const unsigned r = min(row[k], rows - 1), bt = r / a.nh, h = r - bt * a.nh, b = bt / a.Sp, i = bt - b * a.Sp;
-    tok[k] = i;
-    at[k] = (size_t)b * a.nh + h;
+  for (int k = 0; k < kRows; ++k) {
+    const int i = i0 + k * kStep;
     t[k] = 0.0f;
-    if ((int)i < a.S)
+    mdo[k] = mv[k] = __float2half2_rn(0.0f);
+    if (i < a.S)
       for (int c = lane * kEl; c < a.d; c += G * kEl) {
-        const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.o.p) + (size_t)b * a.o.sb +
-                                                        (size_t)i * a.o.st + (size_t)h * a.o.sh + c);
-        const uint4 y = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.dout.p) + (size_t)b * a.dout.sb +
-                                                        (size_t)i * a.dout.st + (size_t)h * a.dout.sh + c);
+        auto at = [&](const AttnView& v) {
+          return *reinterpret_cast<const uint4*>(static_cast<const T*>(v.p) + (size_t)b * v.sb + (size_t)i * v.st +
+                                                 (size_t)h * v.sh + c);
+        };
+        const uint4 x = at(a.o), y = at(a.dout), z = kMax ? at(a.v) : make_uint4(0u, 0u, 0u, 0u);
         const T *xe = reinterpret_cast<const T*>(&x), *ye = reinterpret_cast<const T*>(&y);
 #pragma unroll
         for (int e = 0; e < kEl; ++e) t[k] = fmaf(to_f(xe[e]), to_f(ye[e]), t[k]);
+        if (kMax) {
+          mdo[k] = max_abs(mdo[k], y);
+          mv[k] = max_abs(mv[k], z);
+        }
       }
   }
+  __half2 most = __float2half2_rn(0.0f);                // of dO, of V
 #pragma unroll
-  for (int k = 0; k < kPrepRows; ++k) {
+  for (int k = 0; k < kRows; ++k) {
 #pragma unroll
     for (int w = G / 2; w > 0; w >>= 1) t[k] += __shfl_xor_sync(0xffffffffu, t[k], w);
-    if (row[k] < rows && lane == 0) {
-      const int i = tok[k];
-      float* st = a.stats + at[k] * 2 * a.Sp;
+    const int i = i0 + k * kStep;
+    float lse = INFINITY;
+    if ((lane == 0 || kMax) && i < a.S) lse = a.lse[(size_t)bh * a.S + i];
+    if (lane == 0) {
+      float* st = a.stats + (size_t)bh * 2 * a.Sp;
       const int x = (i >> 6) * 128 + (i & 63);
       constexpr float up = sizeof(T) == 2 ? kAttnPUp : 1.0f, up2 = sizeof(T) == 2 ? 8.0f : 0.0f;   // and its log2
       static_assert(kAttnPUp == 256.0f, "up2 is its logarithm");
-      st[x] = i < a.S ? up2 - a.lse[at[k] * a.S + i] * kAttnLog2e : -INFINITY;
+      st[x] = up2 - lse * kAttnLog2e;
       st[x + 64] = i < a.S ? -t[k] * (1.0f / up) : 0.0f;
+    }
+    if (kMax && i < a.S) {
+      if (lse == INFINITY) mdo[k] = __float2half2_rn(0.0f);
+      if (a.mask && a.mask[(size_t)b * a.S + i] <= kAttnMasked) mv[k] = __float2half2_rn(0.0f);
+      most = __hmax2(most, fold_max(mdo[k], mv[k]));
+    }
+  }
+  if (kMax) {
+    __shared__ __half2 red[kPrepThreads / 32];
+    most = warp_max2(most);
+    if ((tid & 31) == 0) red[tid >> 5] = most;
+    __syncthreads();
+    if (tid == 0) {
+#pragma unroll
+      for (int w = 1; w < kPrepThreads / 32; ++w) most = __hmax2(most, red[w]);
+      a.smax[(size_t)bh * a.nmax + chunk] = most;
     }
   }
 }
@@ -165,9 +184,7 @@ void prep(const AttnOp& a, bool backward, cudaStream_t s) {
   const int nmask = a.mask_seqs * ((a.Sp + kPrepThreads - 1) / kPrepThreads);
   const int nvec = a.vec ? a.nh * ((a.vec_len + kPrepThreads - 1) / kPrepThreads) : 0;
   const int nzero = backward && a.dpart ? 64 : 0;
-  const long long rows = backward ? (long long)a.B * a.Sp * a.nh : 0;
-  constexpr int per = kPrepRows * (kPrepThreads / G);
-  const int nrow = (int)((rows + per - 1) / per);
+  const int nrow = backward ? a.B * a.nh * (a.Sp / (prep_rows(G) * kPrepThreads / G)) : 0;
   launch_pdl(attn_prep_kernel<T, G>, nmask + nvec + nzero + nrow, kPrepThreads, 0, s, a, nmask, nvec, nzero);
   count_launch();
 }
@@ -300,6 +317,10 @@ tl_status plan(const tl_attention* c, bool backward, char* base, AttnOp& a, size
   if (backward) {
     const bool one = attn_one_tile(c->dtype, a.S, a.d);
     if (!one) a.stats = (float*)(base + take(off, (size_t)a.B * a.nh * 2 * a.Sp * 4));
+    if (!one && c->dtype == TL_F16) {
+      a.nmax = a.Sp / attn_prep_rows(a.d);
+      a.smax = (__half2*)(base + take(off, (size_t)a.B * a.nh * a.nmax * sizeof(__half2)));
+    }
     if (c->bias_table) {
       // one row per item of 64 queries (float32), per softmax warp of one of 128, or per (sequence, head)
       a.ditems = c->dtype == TL_F32 ? (a.S + 63) / 64 : one ? 1 : a.Sp / 128 * 8;

@@ -13,6 +13,8 @@
 //   bid    [len]             the bucket of each of those diagonals
 //   stats  [B * heads][Sp / 64][2][64] backward, per 64 queries: -lse2 (-inf for an empty row and past
 //          the end), then -D = -(dO.O); for 16-bit storage log2(kAttnPUp) - lse2 and -D / kAttnPUp
+//   smax   [B * heads][nmax] backward, float16: of each attn_prep_rows(d) tokens the largest |dO| of a row
+//          with a key and the largest |V| of a key that is not removed (ds_factor)
 //   dpart  backward: partial sums of the bias table's gradient, zeroed
 // with Sp = the sequence length rounded up to 128.
 #pragma once
@@ -30,6 +32,46 @@ constexpr float kAttnMasked = -1e30f;      // a mask value at or below this remo
 constexpr int kAttnMaxBuckets = 256;
 constexpr int kAttnFlagKeys = 64;
 constexpr float kAttnPUp = 256.0f;         // 16-bit storage, backward: the factor that P is held at (attention_tc.cu)
+
+// Tokens of a block of attn_prep_kernel's row part: 256 / G groups of G lanes
+// (16 bytes each), prep_rows(G) rows to a group.
+constexpr int kPrepThreads = 256;
+__host__ __device__ constexpr int prep_rows(int G) { return G == 4 ? 2 : 4; }
+inline int attn_prep_rows(int d) { return d * 2 <= 128 ? 128 : 64; }   // 16-bit storage
+
+// float16 storage: dS is held at a power of two chosen per sequence and head,
+// so that gradients of any size (a loss scale, or none) keep its precision:
+// float16 loses bits below 2^-14 and ends at 65504.  |dS_ij| <= P_ij (|dO_i.v_j|
+// + |D_i|) <= 2 M, M := d max|dO| max|V|, and the factor is the power of two F
+// with 2^13 < M F <= 2^14: no overflow (2^15 with room for rounding), and an
+// entry is off by at most 2^-25 / F < 2^-38 M where it is subnormal.  F enters
+// with dP and D and leaves where dQ, dK and the table's gradient are written
+// out; all of it is exact.  m: max|dO| and max|V|.
+__device__ __forceinline__ float ds_factor(__half2 m, int d) {
+  const float M = __low2float(m) * __high2float(m) * (float)d;
+  if (M == 0.0f || isinf(M)) return 1.0f;
+  // 2^e <= M < 2^(e + 1), M from 2^-45 to 2^39
+  const int e = (__float_as_int(M) >> 23) - 127;
+  return __int_as_float((127 + 13 - e) << 23);
+}
+// The larger magnitudes, lane by lane (NaN left out).
+__device__ __forceinline__ __half2 max_abs(__half2 m, uint32_t x) {
+  return __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&x)));
+}
+__device__ __forceinline__ __half2 max_abs(__half2 m, const uint4& x) {
+  return max_abs(max_abs(max_abs(max_abs(m, x.x), x.y), x.z), x.w);
+}
+// The largest of both lanes of a, and of b.
+__device__ __forceinline__ __half2 fold_max(__half2 a, __half2 b) {
+  return __hmax2(__lows2half2(a, b), __highs2half2(a, b));
+}
+__device__ __forceinline__ __half2 warp_max2(__half2 m) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = __hmax2(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+// 1 / x of a power of two.
+__device__ __forceinline__ float inv_pow2(float x) { return __int_as_float((254 << 23) - __float_as_int(x)); }
 
 // A (batch, token, head, dim) tensor: element strides, dim contiguous.
 struct AttnView {
@@ -55,6 +97,8 @@ struct AttnOp {
   int sat;                   // |j - i| >= sat: the bias no longer depends on the distance
   uint8_t* bid;
   float* stats;
+  __half2* smax;             // null but for float16
+  int nmax;
   // bias table gradient: partial sums [B * nh][ditems][buckets], null when not wanted
   float* dpart;
   int ditems;                // partial rows per (b, h)

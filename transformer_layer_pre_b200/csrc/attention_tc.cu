@@ -623,7 +623,8 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
 // probabilities of a long row (1/S each) then stay clear of float16's
 // subnormals, whose rounding is absolute, up to S = 2^22.  The factor comes with
 // -lse2, leaves dS through the product dP / kAttnPUp - D / kAttnPUp, and dV as it
-// is written out; all of it is exact.
+// is written out; all of it is exact.  dS, which has the size of a gradient, is
+// held at a factor of its own for float16 (ds_factor in attention.cuh).
 // TMEM: two or three buffers of S and dP (64 columns each), then the sums: one
 // set of two, or two sets, so that the next item starts while one is written out.
 //
@@ -651,7 +652,7 @@ struct Bwd {
   static constexpr int kAcc = D == 64 && !LONG ? 2 : 1;             // sets of sums
   static constexpr uint32_t kSums = kBuf * 128;                     // their first TMEM column
   static constexpr int kAuxBytes = kVecs + 512 + 16;                // window, two column vectors, description
-  static constexpr int kStAux = 2 * 128 * 4 + 16;                   // row vectors, empty flag
+  static constexpr int kStAux = 2 * 128 * 4 + 16;                   // row vectors, empty flag, dS factor
   static constexpr int kSmem = kSlots * 2 * kSt + 2 * kNs * kMv + kNs * kAuxBytes + kSlots * kStAux +
                                8 * kAttnMaxBuckets * 4 + 8 * kChains * kChain * 4 + 400;
   static constexpr int kBars = 2 * kSlots + 2 * kNs + kFull + 2 * kBuf + 2 * kAcc;
@@ -669,6 +670,9 @@ struct Bwd {
 constexpr int kLongSeq = 1024;
 constexpr int kBwdThreads = 480;
 constexpr int kPauseLoad = 50, kPauseSoft = 20, kPauseStore = 200;   // ns between polls
+
+// Whether dS is held at a factor of its own (float16; bfloat16 has float32's range).
+template <typename T> constexpr bool kHoldsDs = std::is_same<T, half_t>::value;
 
 // Sums the diagonals of a warp's 32 rows x 32 columns (v: this lane's row), as
 // four chains of 8 columns whose steps are independent of one another.  Diagonal
@@ -733,10 +737,11 @@ __device__ __forceinline__ void bin_diagonals(const float* chains, const uint8_t
 
 // A tile's scores and dP, 64 columns of this thread's row, into P and dS.
 // ax: the tile's staged vectors; row: what this row adds (log2 units, bias of
-// a far tile included), nd_row: -D of a query row.
+// a far tile included), nd_row: -D of a query row, F / kAttnPUp in it; up: F /
+// kAttnPUp, with F the factor that dS is held at (ds_factor; 1 for bfloat16).
 template <typename T, bool KEYS, bool NEAR, bool MIX>
 __device__ __forceinline__ void bwd_tile(uint32_t tS, const uint8_t* ax, int win, const float* vecA, const float* vecB,
-                                         float c2, float row, float nd_row, int r, bool grad, float& far_sum,
+                                         float c2, float row, float nd_row, float up, int r, bool grad, float& far_sum,
                                          float* chains, int lane) {
   const int start = 127 - r;   // the row's run of diagonals; copy s is shifted by s + 1
   const float* wnd = reinterpret_cast<const float*>(ax) + (start & 3) * win + (start & ~3);
@@ -760,6 +765,10 @@ __device__ __forceinline__ void bwd_tile(uint32_t tS, const uint8_t* ax, int win
         const float4 w = *reinterpret_cast<const float4*>(vecB + c * 32 + e);
         nd0 = make_float2(w.x, w.y);
         nd1 = make_float2(w.z, w.w);
+        if (kHoldsDs<T>) {
+          nd0 = __fmul2_rn(nd0, f2(up * kAttnPUp));
+          nd1 = __fmul2_rn(nd1, f2(up * kAttnPUp));
+        }
       }
       if (NEAR) {
         const float4 w = *reinterpret_cast<const float4*>(wnd + c * 32 + e);
@@ -769,8 +778,8 @@ __device__ __forceinline__ void bwd_tile(uint32_t tS, const uint8_t* ax, int win
       const float2 x0 = __ffma2_rn(make_float2(s[e], s[e + 1]), f2(c2), add0);
       const float2 x1 = __ffma2_rn(make_float2(s[e + 2], s[e + 3]), f2(c2), add1);
       const float2 p0 = make_float2(ex2f(x0.x), ex2f(x0.y)), p1 = make_float2(ex2f(x1.x), ex2f(x1.y));
-      const float2 d0 = __fmul2_rn(p0, __ffma2_rn(make_float2(dp[e], dp[e + 1]), f2(1.0f / kAttnPUp), nd0));
-      const float2 d1 = __fmul2_rn(p1, __ffma2_rn(make_float2(dp[e + 2], dp[e + 3]), f2(1.0f / kAttnPUp), nd1));
+      const float2 d0 = __fmul2_rn(p0, __ffma2_rn(make_float2(dp[e], dp[e + 1]), f2(up), nd0));
+      const float2 d1 = __fmul2_rn(p1, __ffma2_rn(make_float2(dp[e + 2], dp[e + 3]), f2(up), nd1));
       if (KEYS) {
         wp[e / 2] = pack2<T>(p0.x, p0.y);
         wp[e / 2 + 1] = pack2<T>(p1.x, p1.y);
@@ -841,12 +850,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   };
   auto row_vec = [&](int n) { return reinterpret_cast<float*>(sStAux + (n % C::kSlots) * C::kStAux); };
   auto none_flag = [&](int n) { return reinterpret_cast<int*>(sStAux + (n % C::kSlots) * C::kStAux + 1024); };
+  auto factor = [&](int n) { return reinterpret_cast<float*>(sStAux + (n % C::kSlots) * C::kStAux + 1028); };
 
   if (warp == 12) {
     // ---- producer
     uint32_t g = 0, st_issued = 0;
     int n = 0;
     bool ok = true;
+    // the first of an item's magnitudes, read one item ahead
+    auto first_max = [&](int it) {
+      const int bh = (it < items ? it : it - items) / nr;
+      return it < 2 * items && lane < a.nmax ? a.smax[(size_t)bh * a.nmax + lane] : __float2half2_rn(0.0f);
+    };
+    __half2 most = kHoldsDs<T> ? first_max(blockIdx.x) : __float2half2_rn(0.0f);
     for (int it = blockIdx.x; it < 2 * items && ok; it += gridDim.x, ++n) {
       const bool keys = it < items;
       const int x = keys ? it : it - items, bh = x / nr, ri = x - bh * nr, b = bh / a.nh, h = bh - b * a.nh;
@@ -860,8 +876,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       int j = keys ? (flags[2 * ri] == 2 && flags[2 * ri + 1] == 2 ? nm : 0) : tiles.next(0, mix);
       const bool none = j == nm;
       const int slot = n % C::kSlots;
+      float F = 1.0f;
+      if (kHoldsDs<T>) {
+        __half2 m = most;
+        for (int c = 32 + lane; c < a.nmax; c += 32) m = __hmax2(m, a.smax[(size_t)bh * a.nmax + c]);
+        F = ds_factor(warp_max2(m), a.d);
+        most = first_max(it + gridDim.x);
+      }
       if (lane == 0 && (ok = wait_bar<kPauseLoad>(&st_empty[slot], ((n / C::kSlots) & 1) ^ 1, err, 301))) {
         *none_flag(n) = none;
+        *factor(n) = F;
         ++st_issued;
         mbar_arrive_expect_tx(&st_full[slot], 2 * C::kSt + (keys ? 512 : 1024));
         uint8_t* st = sSt + slot * 2 * C::kSt;
@@ -1016,11 +1040,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       uint8_t* st = sSt + slot * 2 * C::kSt;
       ok = wait_warp<kPauseStore>(&st_full[slot], (n / C::kSlots) & 1, err, 321);
       const bool none = ok && *none_flag(n) != 0;
+      const float F = kHoldsDs<T> && ok ? *factor(n) : 1.0f;
       if (ok && (ok = wait_warp<kPauseStore>(&acc_full[ab], (n / C::kAcc) & 1, err, 322))) {
         tc_fence_after();
 #pragma unroll 1
         for (int q = 0; q < (keys ? 2 : 1); ++q) {
-          const float f = q == 0 ? a.scale : 1.0f / kAttnPUp;
+          const float f = q == 0 ? a.scale * inv_pow2(F) : 1.0f / kAttnPUp;
           uint8_t* out = st + q * C::kSt;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -1074,6 +1099,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     size_t part = 0;               // this warp's row of dpart for the current item
     bool grad = false, any_far = false;
     float add = 0.0f, nd = 0.0f, far_behind = 0.0f, far_ahead = 0.0f;
+    float up = 1.0f / kAttnPUp;
     // the item's bias gradient: this warp's share
     auto flush = [&]() {
       if (any_far) {
@@ -1087,7 +1113,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         any_far = false;
       }
       for (int u = lane; u < a.buckets; u += 32) {
-        a.dpart[part + u] = bins[u];
+        a.dpart[part + u] = kHoldsDs<T> ? bins[u] * inv_pow2(up * kAttnPUp) : bins[u];
         bins[u] = 0.0f;
       }
       __syncwarp();
@@ -1110,6 +1136,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const float* rv = row_vec(cur);
         add = rv[keys ? r : (r >> 6) * 128 + (r & 63)];
         nd = keys ? 0.0f : rv[(r >> 6) * 128 + 64 + (r & 63)];
+        if (kHoldsDs<T>) {
+          const float F = *factor(cur);
+          up = F * (1.0f / kAttnPUp);
+          nd *= F;
+        }
         grad = want && !keys;
         const int x = (int)(blockIdx.x + (unsigned)cur * gridDim.x) - (keys ? 0 : items);
         const int bh = x / nr, ri = x - bh * nr;
@@ -1125,14 +1156,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const float row = add + t.bias;
         float far = 0.0f;
         if (keys) {
-          if (t.bits & kNear) bwd_tile<T, true, true, false>(tS, ax, kWin, va, vb, c2, row, nd, r, false, far, chains, lane);
-          else bwd_tile<T, true, false, false>(tS, ax, kWin, va, vb, c2, row, nd, r, false, far, chains, lane);
+          if (t.bits & kNear) bwd_tile<T, true, true, false>(tS, ax, kWin, va, vb, c2, row, nd, up, r, false, far, chains, lane);
+          else bwd_tile<T, true, false, false>(tS, ax, kWin, va, vb, c2, row, nd, up, r, false, far, chains, lane);
         } else if (t.bits & kNear) {
-          bwd_tile<T, false, true, true>(tS, ax, kWin, va, vb, c2, row, nd, r, grad, far, chains, lane);
+          bwd_tile<T, false, true, true>(tS, ax, kWin, va, vb, c2, row, nd, up, r, grad, far, chains, lane);
         } else if (t.bits & kMixed) {
-          bwd_tile<T, false, false, true>(tS, ax, kWin, va, vb, c2, row, nd, r, grad, far, chains, lane);
+          bwd_tile<T, false, false, true>(tS, ax, kWin, va, vb, c2, row, nd, up, r, grad, far, chains, lane);
         } else {
-          bwd_tile<T, false, false, false>(tS, ax, kWin, va, vb, c2, row, nd, r, grad, far, chains, lane);
+          bwd_tile<T, false, false, false>(tS, ax, kWin, va, vb, c2, row, nd, up, r, grad, far, chains, lane);
         }
         if (!(t.bits & kNear)) {
           any_far = true;
@@ -1181,7 +1212,7 @@ struct One {
   static constexpr int kThreads = 256;
   static constexpr int kWin = 264;                // floats of a window copy: 256 diagonals, 8 banks apart
   static constexpr int kChainFloats = 8 * kChains * kChain;
-  static constexpr int kSmem = 5 * kRegion + 4 * kWin * 4 + 2 * 128 * 4 + 8 * kAttnMaxBuckets * 4 + kChainFloats * 4 + 48;
+  static constexpr int kSmem = 5 * kRegion + 4 * kWin * 4 + 2 * 128 * 4 + 8 * kAttnMaxBuckets * 4 + kChainFloats * 4 + 32 + 48;
 };
 static_assert(2 * (One::kSmem + 1024) <= 228 * 1024, "two blocks do not fit an SM's shared memory");
 
@@ -1201,7 +1232,8 @@ __global__ void __launch_bounds__(One::kThreads, 2)
   float* vecB = vecA + 128;                                           // -D / kAttnPUp
   float* sBins = vecB + 128;
   float* sChains = sBins + 8 * kAttnMaxBuckets;
-  uint64_t* bar = reinterpret_cast<uint64_t*>(sChains + One::kChainFloats);
+  __half2* sMax = reinterpret_cast<__half2*>(sChains + One::kChainFloats);  // per warp, largest |dO| and |V|
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sMax + 8);
   uint64_t *qk_full = bar, *vd_full = bar + 1, *o_full = bar + 2, *s_done = bar + 3, *sums_done = bar + 4;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 5);
 
@@ -1232,6 +1264,7 @@ __global__ void __launch_bounds__(One::kThreads, 2)
   }
   auto bin = [&] { bin_diagonals<-1>(chains, a.bid + a.vec_off - half * 64 + (warp & 3) * 32, bins, lane); };
   bool ok = true;
+  float F = 1.0f;                                                     // what dS is held at
   if (!none) {
     if (tid == 0) {
       mbar_arrive_expect_tx(qk_full, 2 * kRegion);
@@ -1249,6 +1282,7 @@ __global__ void __launch_bounds__(One::kThreads, 2)
     const int row = tid >> 1, part = tid & 1;                           // D: two threads to a query
     const float lse = part && row < a.S ? a.lse[(size_t)bh * a.S + row] : 0.0f;
     const float mask = a.maskx[(size_t)mb * a.Sp + r];
+    const bool gone = kHoldsDs<T> && a.maskx[(size_t)mb * a.Sp + row] == -INFINITY;
     if (tid == 0) {
       const uint32_t id = idesc_f16(128, 128, std::is_same<T, bf16_t>::value, false, false);
       const uint64_t dq = desc_k(smem_u32(sQ), 0, kRegion), dk = desc_k(smem_u32(sK), 0, kRegion),
@@ -1266,6 +1300,7 @@ __global__ void __launch_bounds__(One::kThreads, 2)
     ok = wait_warp<kPauseSoft>(vd_full, 0, err, 403) && ok;
     ok = wait_warp<kPauseSoft>(o_full, 0, err, 404) && ok;
     float d = 0.0f;
+    __half2 mdo = __float2half2_rn(0.0f), mv = mdo;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int at = row * 128 + (((part * 4 + j) ^ (row & 7)) << 4);
@@ -1273,11 +1308,28 @@ __global__ void __launch_bounds__(One::kThreads, 2)
       const T *xe = reinterpret_cast<const T*>(&x), *ye = reinterpret_cast<const T*>(&y);
 #pragma unroll
       for (int e = 0; e < 8; ++e) d = fmaf(to_f(xe[e]), to_f(ye[e]), d);
+      if (kHoldsDs<T>) {
+        mdo = max_abs(mdo, y);
+        mv = max_abs(mv, *reinterpret_cast<const uint4*>(sV + at));
+      }
     }
     d += __shfl_xor_sync(0xffffffffu, d, 1);
     if (part) vecA[row] = row < a.S ? 8.0f - lse * kAttnLog2e : -INFINITY;
     else vecB[row] = -d * (1.0f / kAttnPUp);
+    if (kHoldsDs<T>) {
+      // a sequence with a key has no empty row; rows past the end were read as 0
+      if (gone) mv = __float2half2_rn(0.0f);
+      const __half2 m = warp_max2(fold_max(mdo, mv));
+      if (lane == 0) sMax[warp] = m;
+    }
     __syncthreads();
+    if (kHoldsDs<T>) {
+      __half2 m = sMax[0];
+#pragma unroll
+      for (int w = 1; w < 8; ++w) m = __hmax2(m, sMax[w]);
+      F = ds_factor(m, a.d);
+    }
+    const float up = F * (1.0f / kAttnPUp);
     ok = wait_warp<kPauseSoft>(s_done, 0, err, 405) && ok;
     tc_fence_after();
 
@@ -1306,9 +1358,10 @@ __global__ void __launch_bounds__(One::kThreads, 2)
         const float2 x0 = __ffma2_rn(make_float2(s[e], s[e + 1]), f2(a.c2), add0);
         const float2 x1 = __ffma2_rn(make_float2(s[e + 2], s[e + 3]), f2(a.c2), add1);
         const float2 p0 = make_float2(ex2f(x0.x), ex2f(x0.y)), p1 = make_float2(ex2f(x1.x), ex2f(x1.y));
-        const float2 d0 = __fmul2_rn(p0, __ffma2_rn(make_float2(dp[e], dp[e + 1]), f2(1.0f / kAttnPUp), make_float2(n.x, n.y)));
-        const float2 d1 =
-            __fmul2_rn(p1, __ffma2_rn(make_float2(dp[e + 2], dp[e + 3]), f2(1.0f / kAttnPUp), make_float2(n.z, n.w)));
+        float2 nd0 = make_float2(n.x, n.y), nd1 = make_float2(n.z, n.w);
+        if (kHoldsDs<T>) nd0 = __fmul2_rn(nd0, f2(F)), nd1 = __fmul2_rn(nd1, f2(F));
+        const float2 d0 = __fmul2_rn(p0, __ffma2_rn(make_float2(dp[e], dp[e + 1]), f2(up), nd0));
+        const float2 d1 = __fmul2_rn(p1, __ffma2_rn(make_float2(dp[e + 2], dp[e + 3]), f2(up), nd1));
         wp[e / 2] = pack2<T>(p0.x, p0.y);
         wp[e / 2 + 1] = pack2<T>(p1.x, p1.y);
         wd[e / 2] = pack2<T>(d0.x, d0.y);
@@ -1356,7 +1409,7 @@ __global__ void __launch_bounds__(One::kThreads, 2)
     const uint32_t col = k == 2 ? 192 + half * 32 : (half ? 128 : 32) + k * 32;
     uint8_t* out = k == 2 ? sK : (half ? sQ : sDo);
     const int c = k == 2 ? half : k;
-    const float f = k == 2 || half ? a.scale : 1.0f / kAttnPUp;
+    const float f = k == 2 || half ? a.scale * inv_pow2(F) : 1.0f / kAttnPUp;
     float v[32];
     tmem_ld32_nowait(tmem + ((uint32_t)((warp & 3) * 32) << 16) + col, v);
     tmem_ld_wait();
@@ -1387,7 +1440,7 @@ __global__ void __launch_bounds__(One::kThreads, 2)
       float t = 0.0f;
 #pragma unroll
       for (int w = 0; w < 8; ++w) t += sBins[w * kAttnMaxBuckets + u];
-      a.dpart[(size_t)bh * a.buckets + u] = t;
+      a.dpart[(size_t)bh * a.buckets + u] = t * inv_pow2(F);
     }
   }
   if (tid == 0) {
