@@ -196,7 +196,11 @@ struct LiveTiles {
 // when O was last rescaled; O and the row sum are rescaled only once the
 // maximum has grown by more than 2^8, so P stays below 256 and most tiles
 // skip it.  P is rounded to the storage type (at most half a step, relative)
-// for its product with V; the row sum takes the unrounded P.
+// for its product with V; the row sum takes the unrounded P.  P and the row sum
+// are held 2^7 times too large (exact; O / l does not see it, lse takes it out):
+// float16's subnormals, whose rounding is absolute, then begin at 2^-21 of the
+// row's maximum instead of 2^-14, and what 2^20 small probabilities lose there
+// is at most 2^-12 of the largest |V|.
 //
 // The bias is one number for a tile beyond the last bucket's border; else the
 // tile's 255 diagonals are staged as four copies shifted by one float each, so
@@ -229,7 +233,7 @@ struct Fwd {
 static_assert(4 * (Fwd<64>::kSmem + 1024) <= 228 * 1024 && 2 * (Fwd<128>::kSmem + 1024) <= 228 * 1024,
               "the blocks of an SM do not fit its shared memory");
 constexpr int kFwdThreads = 192;
-constexpr float kRescale = 8.0f;
+constexpr float kRescale = 8.0f, kFwdUp = 7.0f;   // log2: P < 2^15 in float16
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
@@ -529,7 +533,7 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
 #pragma unroll 1
           for (int c = 0; c < D; c += 8) tmem_scale8(tmem + lo + C::kO + c, f);
         }
-        const float sub = add - (ref == -INFINITY ? 0.0f : ref);
+        const float sub = add - (ref == -INFINITY ? 0.0f : ref) + kFwdUp;
         float2 sum0 = f2(0.0f), sum1 = f2(0.0f);
 #pragma unroll 1
         for (int c = 0; c < C::kTK / 32; ++c) {
@@ -582,7 +586,7 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
         }
         tc_fence_before();
         const int row = i * 128 + r;
-        if (row < a.S) a.lse[(size_t)bh * a.S + row] = l == 0.0f ? INFINITY : (ref + log2f(l)) * kAttnLn2;
+        if (row < a.S) a.lse[(size_t)bh * a.S + row] = l == 0.0f ? INFINITY : (ref + (log2f(l) - kFwdUp)) * kAttnLn2;
         fence_proxy_async_smem();
       }
       // each warp times its own waits: all four go on, or none does
