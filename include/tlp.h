@@ -305,10 +305,13 @@ tl_status tl_bias_grad_noalloc(int dtype, const void* dz, int rows, int cols, fl
  * tl_heads: a (batch, seq, heads, head_dim) tensor by its element strides;
  * the head_dim entries of one head are contiguous.  data is 16-byte aligned,
  * and the strides of every dimension of more than one entry are multiples of
- * 16 bytes and at least head_dim (those of one entry are ignored).  Outputs
- * must not overlap anything else, and each of an output's dimensions steps over
- * all of those with smaller strides (TL_EINVAL); elements between their rows
- * are left alone.
+ * 16 bytes and at least head_dim (those of one entry are ignored).  Outputs,
+ * lse, dtable and the workspace among them, must not share memory with any
+ * other tensor of the call, and each of an output's dimensions steps over all of
+ * those with smaller strides (both TL_EINVAL).  Inputs and outputs may be views
+ * that interleave within one buffer; elements between an output's rows are left
+ * alone.  (Tensors of different strides within one another's span for which
+ * that would take more than 2^16 steps to find out are refused.)
  * lse: (batch, heads, seq) float32, dense.  bias_table: (buckets, heads),
  * dense, storage dtype; dtable: the same shape, float32, overwritten, or added
  * to when `accumulate` is not 0; NULL when its gradient is not wanted.

@@ -10,6 +10,7 @@
 #include "../../include/tlp.h"
 #include "attention.cuh"
 #include "kernels.h"
+#include "overlap.h"
 #include "profile.h"
 
 namespace tlp {
@@ -331,7 +332,22 @@ tl_status plan(const tl_attention* c, bool backward, char* base, AttnOp& a, size
   return TL_OK;
 }
 
-bool same(const tl_heads* x, const tl_heads* y) { return x->data == y->data; }
+// Whether every output (the first `outs`) is apart from every other tensor.
+bool apart(const ByteRows* x, int outs, int n) {
+  for (int i = 0; i < outs; ++i)
+    for (int j = i + 1; j < n; ++j)
+      if (overlap(x[i], x[j])) return false;
+  return true;
+}
+ByteRows rows_of(const tl_heads* v, const tl_attention* c) {
+  return ByteRows(v->data, v->batch, c->batch, v->token, c->seq, v->head, c->heads, c->head_dim, (int)dtype_size(c->dtype));
+}
+// The dense ones; an absent one is empty.
+ByteRows lse_rows(const float* lse, const tl_attention* c) { return ByteRows(lse, (int64_t)c->batch * c->heads * c->seq * 4); }
+ByteRows mask_rows(const tl_attention* c) { return ByteRows(c->mask, c->mask ? (int64_t)c->batch * c->seq * 4 : 0); }
+ByteRows table_rows(const void* t, const tl_attention* c, size_t es) {
+  return ByteRows(t, t ? (int64_t)c->buckets * c->heads * (int64_t)es : 0);
+}
 
 }  // namespace
 
@@ -369,9 +385,12 @@ tl_status tl_attention_forward(const tl_attention* c, const tl_heads* q, const t
   const tl_heads* all[4] = {q, k, v, o};
   for (const tl_heads* t : all)
     if (!view_ok(t, c->dtype, a.B, a.S, a.nh, a.d)) return TL_EINVAL;
-  if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3) || same(o, q) || same(o, k) || same(o, v)) return TL_EINVAL;
+  if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3)) return TL_EINVAL;
   if (!disjoint(o, a.B, a.S, a.nh, a.d)) return TL_EINVAL;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < need) return TL_EINVAL;
+  const ByteRows parts[8] = {rows_of(o, c), lse_rows(lse, c), ByteRows(workspace, (int64_t)need), rows_of(q, c),
+                             rows_of(k, c), rows_of(v, c), mask_rows(c), table_rows(c->bias_table, c, dtype_size(c->dtype))};
+  if (!apart(parts, 3, 8)) return TL_EINVAL;
   if (cudaGetLastError() != cudaSuccess) return TL_ECUDA;
   a.q = view(q, a.B, a.S, a.nh, a.d);
   a.k = view(k, a.B, a.S, a.nh, a.d);
@@ -398,14 +417,16 @@ tl_status tl_attention_backward(const tl_attention* c, const tl_heads* q, const 
   const tl_heads* all[8] = {q, k, v, o, dout, dq, dk, dv};
   for (const tl_heads* t : all)
     if (!view_ok(t, c->dtype, a.B, a.S, a.nh, a.d)) return TL_EINVAL;
-  for (int i = 5; i < 8; ++i) {
+  for (int i = 5; i < 8; ++i)
     if (!disjoint(all[i], a.B, a.S, a.nh, a.d)) return TL_EINVAL;
-    for (int j = 0; j < i; ++j)
-      if (same(all[i], all[j])) return TL_EINVAL;
-  }
   if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3)) return TL_EINVAL;
   if (dtable && (!c->bias_table || (reinterpret_cast<uintptr_t>(dtable) & 3))) return TL_EINVAL;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < need) return TL_EINVAL;
+  const ByteRows parts[13] = {rows_of(dq, c), rows_of(dk, c), rows_of(dv, c), table_rows(dtable, c, 4),
+                              ByteRows(workspace, (int64_t)need), rows_of(q, c), rows_of(k, c), rows_of(v, c), rows_of(o, c),
+                              rows_of(dout, c), lse_rows(lse, c), mask_rows(c),
+                              table_rows(c->bias_table, c, dtype_size(c->dtype))};
+  if (!apart(parts, 5, 13)) return TL_EINVAL;
   if (cudaGetLastError() != cudaSuccess) return TL_ECUDA;
   a.q = view(q, a.B, a.S, a.nh, a.d);
   a.k = view(k, a.B, a.S, a.nh, a.d);
