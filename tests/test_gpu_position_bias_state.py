@@ -1,0 +1,61 @@
+"""What a refused position bias leaves behind, in the layer and in the stack; the stack's bias on a stream of the
+caller's; the exchange of the shared table's gradient."""
+import os
+import subprocess
+import sys
+
+import pytest
+import torch
+
+import transformer_layer_pre_b200 as tlp
+from transformer_layer_pre_b200 import Layer
+from transformer_layer_pre_b200.dp import gradient_shapes
+
+pytestmark = pytest.mark.gpu
+TL_ENOMEM = 2
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def _weights(h, f, g, dtype=torch.float16):
+    return {n: (0.1 * torch.randn(s, generator=g, device="cuda")).to(dtype) for n, s in gradient_shapes(h, f).items()}
+
+
+CHILD = """
+import torch
+import transformer_layer_pre_b200 as tlp
+from test_gpu_position_bias_state import _weights, TL_ENOMEM
+g = torch.Generator(device="cuda").manual_seed(3)
+wt = _weights(64, 64, g)
+x = torch.randn(1, 304, 64, generator=g, device="cuda").half()
+small, large = (torch.randn(n, 1, generator=g, device="cuda").half() for n in (4, 256))
+layer = tlp.Layer(1, 304, 64, 1, 64, dtype=torch.float16)
+layer.set_position_bias(small, 100)
+before = layer.forward(x, None, wt).clone()
+plain = tlp.Layer(1, 304, 64, 1, 64, dtype=torch.float16).forward(x, None, wt)
+torch.cuda.synchronize()
+status = None
+graph = torch.cuda.CUDAGraph()
+try:
+    with torch.cuda.graph(graph):          # an allocation is an error while a stream is captured
+        try:
+            layer.set_position_bias(large, 100)
+        except tlp.TlError as e:
+            status = e.status
+except Exception:
+    pass                                   # the capture is broken off
+torch.cuda.synchronize()
+after = layer.forward(x, None, wt)
+torch.cuda.synchronize()
+assert status == TL_ENOMEM, status
+assert not torch.equal(before, plain) and torch.equal(before, after)
+layer.set_position_bias(large, 100)
+assert not torch.equal(before, layer.forward(x, None, wt))
+tlp.device_check()
+print("kept")
+"""
+
+
+def test_a_failed_allocation_keeps_the_bias():
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([ROOT, os.path.join(ROOT, "tests")]))
+    r = subprocess.run([sys.executable, "-c", CHILD], capture_output=True, text=True, timeout=300, env=env, cwd=ROOT)
+    assert r.returncode == 0 and "kept" in r.stdout, r.stdout + r.stderr

@@ -512,12 +512,13 @@ tl_status layer_set_position_bias(tl_layer* L, const void* table, int buckets, i
   tl_status st = ensure_buffers(L);
   if (st != TL_OK) return st;
   if (L->bias_ws_bytes < need) {
-    free_bias(L);
-    if (cudaMalloc(&L->bias_ws, need) != cudaSuccess) {
+    void* ws = nullptr;
+    if (cudaMalloc(&ws, need) != cudaSuccess) {
       cudaGetLastError();
-      L->bias_ws = nullptr;
       return fail(L, TL_ENOMEM, "cudaMalloc of the position bias workspace failed");
     }
+    free_bias(L);   // only now: a call that fails leaves the layer as it was
+    L->bias_ws = ws;
     L->bias_ws_bytes = need;
   }
   L->bias = c;
