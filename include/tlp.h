@@ -189,11 +189,12 @@ tl_status layer_share_scratch(tl_layer* layer, void* scratch, size_t bytes);
  * added to when `accumulate` is not 0 (one table shared by the layers of a
  * stack: zero it first).  Both are read and written by later calls and must
  * stay valid; table NULL takes the bias away (the other arguments are ignored).
- * The layer allocates a workspace of its own for it (TL_ENOMEM).  A call that
- * fails changes nothing.  Discards the saved activations, and layer_set_options takes the bias away.  TL_EINVAL for
- * buckets or a distance that tl_attention refuses.  Attention dropout has no
- * place in these kernels: with attn_dropout > 0 a training-mode forward returns
- * TL_EUNSUPPORTED (inference is served). */
+ * The layer allocates a workspace of its own for it (TL_ENOMEM).  TL_EINVAL for
+ * buckets or a distance that tl_attention refuses, TL_EUNSUPPORTED for a layer
+ * beyond its sizes.  A call that fails changes nothing; one that succeeds
+ * discards the saved activations, and layer_set_options takes the bias away.
+ * Attention dropout has no place in these kernels: with attn_dropout > 0 a
+ * training-mode forward returns TL_EUNSUPPORTED (inference is served). */
 tl_status layer_set_position_bias(tl_layer* layer, const void* table, int buckets, int max_distance,
                                   float* dtable, int accumulate);
 

@@ -506,7 +506,11 @@ tl_status layer_set_position_bias(tl_layer* L, const void* table, int buckets, i
   static const float kMask = 0.0f;
   c.mask = &kMask;
   const size_t need = tl_attention_workspace_bytes(&c, 1);
-  if (!need) return fail(L, TL_EINVAL, "position bias: buckets even, 4 to 256, buckets/4 < max_distance <= 2^20");
+  if (!need) {
+    if (L->S > (1 << 20) || (long long)L->B * L->nh * ((L->S + 127) / 128 * 128) > (1ll << 30))
+      return fail(L, TL_EUNSUPPORTED, "position bias: seq up to 2^20, batch * heads * (seq rounded up to 128) up to 2^30");
+    return fail(L, TL_EINVAL, "position bias: an aligned table, buckets even, 4 to 256, buckets/4 < max_distance <= 2^20");
+  }
   if (reinterpret_cast<uintptr_t>(dtable) & 3) return fail(L, TL_EINVAL, "dtable must be 4-byte aligned");
   c.mask = nullptr;
   tl_status st = ensure_buffers(L);
