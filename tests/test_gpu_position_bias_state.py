@@ -59,3 +59,18 @@ def test_a_failed_allocation_keeps_the_bias():
     env = dict(os.environ, PYTHONPATH=os.pathsep.join([ROOT, os.path.join(ROOT, "tests")]))
     r = subprocess.run([sys.executable, "-c", CHILD], capture_output=True, text=True, timeout=300, env=env, cwd=ROOT)
     assert r.returncode == 0 and "kept" in r.stdout, r.stdout + r.stderr
+
+
+def test_a_table_on_another_device_than_the_current_one(monkeypatch):
+    """The layer works on the current device (its own, or an error); a table elsewhere is no table of it."""
+    layer = Layer(1, 16, 64, 1, 64, dtype=torch.float16)
+    try:
+        table = torch.zeros(32, 1, dtype=torch.float16, device="cuda")
+        layer.set_position_bias(table)
+        other = table.get_device() + 1
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: other)
+        with pytest.raises(tlp.TlError, match="device"):
+            layer.set_position_bias(table)
+    finally:
+        monkeypatch.undo()
+        layer.close()

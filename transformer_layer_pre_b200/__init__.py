@@ -258,8 +258,8 @@ class Layer:
         if dtable is not None and (dtable.shape != table.shape or dtable.dtype != torch.float32
                                    or dtable.device != table.device or not dtable.is_contiguous()):
             _fail("dtable must be a contiguous float32 tensor of table's shape on its device")
-        if not table.is_cuda:
-            _fail("table must be on the layer's device")
+        if not table.is_cuda or table.get_device() != torch.cuda.current_device():
+            _fail("table must be on the current device, which has to be the layer's")
         self._check(self.lib.layer_set_position_bias(self.handle, _ptr(table), table.shape[0], max_distance,
                                                      _ptr(dtable), int(accumulate)))
         self._bias_ref = (table, dtable)
