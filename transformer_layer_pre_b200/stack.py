@@ -77,18 +77,33 @@ class EncoderStack:
         self.keep: list = [True] * num_layers
         self.heads = heads
         self.table_grad: _TableGrad | None = None
+        self._bias: tuple | None = None          # table, max_distance, table_grad
 
     def set_position_bias(self, table, max_distance: int = 128) -> None:
         """One relative position bias table, (buckets, heads) in the stack's
         dtype, for the attention of every layer (None: no bias); its float32
         gradient is `position_bias_grad`, overwritten by each backward.  Needs
         attn_dropout 0 in training."""
-        self.table_grad = None if table is None else _TableGrad(table)
-        for layer in self.layers:
-            if table is None:
-                layer.set_position_bias(None)
-            else:
-                layer.set_position_bias(table, max_distance, self.table_grad.flat, accumulate=True)
+        new = None if table is None else (table, max_distance, _TableGrad(table))
+        taken = []
+        try:
+            for layer in self.layers:
+                self._give_bias(layer, new)
+                taken.append(layer)
+        except Exception:
+            for layer in taken:          # a refused table leaves the earlier one in every layer
+                self._give_bias(layer, self._bias)
+            raise
+        self._bias = new
+        self.table_grad = None if new is None else new[2]
+
+    @staticmethod
+    def _give_bias(layer, bias) -> None:
+        if bias is None:
+            layer.set_position_bias(None)
+        else:
+            table, max_distance, grad = bias
+            layer.set_position_bias(table, max_distance, grad.flat, accumulate=True)
 
     @property
     def position_bias_grad(self):
