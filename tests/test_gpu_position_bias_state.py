@@ -74,3 +74,44 @@ def test_a_table_on_another_device_than_the_current_one(monkeypatch):
     finally:
         monkeypatch.undo()
         layer.close()
+
+
+def test_stack_on_a_stream_of_the_callers_with_an_exchange():
+    """Forward, backward and clipping on an explicit stream, with a stand-in collective that adds an identical rank: the
+    bits of the step on the current stream, the table's gradient exchanged last and after it was written."""
+    from transformer_layer_pre_b200.dp import GradExchanger
+    from transformer_layer_pre_b200.stack import EncoderStack
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x, dy = (torch.randn(2, 200, 128, generator=g, device="cuda").half() for _ in range(2))
+    wts = [_weights(128, 256, g) for _ in range(2)]
+    table = torch.randn(32, 2, generator=g, device="cuda").half()
+    st = EncoderStack(2, 2, 200, 128, 2, 256, dtype=torch.float16)
+    seen = []
+
+    def identical_rank(t):
+        torch.cuda._sleep(20_000_000)            # a slow collective
+        seen.append(t.clone())
+        t.add_(t)
+
+    def results():
+        torch.cuda.synchronize()
+        return [t.clone() for t in (y, dx, norm, st.position_bias_grad, *(f.flat for f in st.grads))]
+
+    try:
+        st.set_position_bias(table)
+        y = st.forward(x, None, wts)
+        dx, _ = st.backward(dy, wts)
+        unclipped = st.position_bias_grad.clone()
+        norm = st.clip_grad_norm(0.5)
+        want = results()
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        for _ in range(2):
+            y = st.forward(x, None, wts, stream=stream)
+            dx, _ = st.backward(dy, wts, exchange=GradExchanger(allreduce=identical_rank, world=2), stream=stream)
+            norm = st.clip_grad_norm(0.5, stream=stream)
+            assert all(torch.equal(a, b) for a, b in zip(results(), want))
+        assert len(seen) == 6 and torch.equal(seen[2], unclipped) and torch.equal(seen[5], unclipped)
+        tlp.device_check()
+    finally:
+        st.close()
