@@ -405,6 +405,9 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
           }
           const int ks = kc % C::kKv;
           const uint32_t kp = (kc / C::kKv) & 1;
+          // S goes over the P that the last product read, and products with
+          // different accumulators may overtake one another
+          if (kc > 0 && !(ok = wait_bar<0>(&v_empty[(kc - 1) % C::kKv], ((kc - 1) / C::kKv) & 1, err, 217))) break;
           ++kc;
           tc_fence_after();
 #pragma unroll
