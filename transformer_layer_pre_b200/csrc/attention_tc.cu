@@ -632,8 +632,8 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
 // -lse2, leaves dS through the product dP / kAttnPUp - D / kAttnPUp, and dV as it
 // is written out; all of it is exact.  dS, which has the size of a gradient, is
 // held at a factor of its own for float16 (ds_factor in attention.cuh).
-// TMEM: two or three buffers of S and dP (64 columns each), then the sums: one
-// set of two, or two sets, so that the next item starts while one is written out.
+// TMEM: three (head dim 128: two) buffers of S and dP, 64 columns each, then the
+// two sums.
 //
 // Bound: the chain of a tile (operands, product, exponentials, product) through
 // the barriers between its warps: tensor pipe 33 %, exponentials 38 %, issue
@@ -649,32 +649,33 @@ struct Bwd {
   static constexpr int kSt = D / 64 * kRegion;                      // a stationary tile
   static constexpr int kMvRegion = 64 * 128;
   static constexpr int kMv = D / 64 * kMvRegion;                    // a moving tile
-  static constexpr int kSlots = D == 128 && LONG ? 1 : 2;           // stationary pairs
+  static_assert(D == 128 || !LONG, "head dim 128 alone has two forms");
+  static constexpr int kSlots = LONG ? 1 : 2;                       // stationary pairs
   static constexpr int kNs = D == 64 || LONG ? 4 : 2;               // moving pairs
-  static constexpr int kBuf = D == 64 && LONG ? 3 : 2;              // S, dP buffers
+  static constexpr int kBuf = D == 64 ? 3 : 2;                      // S, dP buffers
   // Barriers of finished scores.  Two groups take the tiles in turn, and a wait
   // for a parity cannot tell the phase before the last one done from its own: a
   // barrier belongs to one group, which then waits for each of its phases.
   static constexpr int kFull = kBuf % 2 ? 2 * kBuf : kBuf;
-  static constexpr int kAcc = D == 64 && !LONG ? 2 : 1;             // sets of sums
   static constexpr uint32_t kSums = kBuf * 128;                     // their first TMEM column
   static constexpr int kAuxBytes = kVecs + 512 + 16;                // window, two column vectors, description
   static constexpr int kStAux = 2 * 128 * 4 + 16;                   // row vectors, empty flag, dS factor
   static constexpr int kSmem = kSlots * 2 * kSt + 2 * kNs * kMv + kNs * kAuxBytes + kSlots * kStAux +
                                8 * kAttnMaxBuckets * 4 + 8 * kChains * kChain * 4 + 400;
-  static constexpr int kBars = 2 * kSlots + 2 * kNs + kFull + 2 * kBuf + 2 * kAcc;
+  static constexpr int kBars = 2 * kSlots + 2 * kNs + kFull + 2 * kBuf + 2;
   static_assert(kFull % 2 == 0, "a barrier of finished scores serves both softmax groups");
   static_assert(kBars * 8 + 4 <= 400, "the barriers do not fit their shared memory");
-  static_assert(kSums + kAcc * 2 * D <= 512, "the sums do not fit the tensor memory");
+  static_assert(kSums + 2 * D <= 512, "the sums do not fit the tensor memory");
   static_assert(kSmem <= 227 * 1024, "the backward's shared memory exceeds a block's maximum");
 };
-// LONG, from this length on: for D = 128 one stationary pair and four moving
-// ones instead of two and two (shared memory holds six), for D = 64 a third
-// buffer of S and dP instead of a second set of sums.  B4 h8 d128 S2048: 310 us
-// against 344; B4 h16 d64 S2048: 409 against 434.  Short sequences, whose items
-// are over sooner, lose by it: B8 h8 d128 S512 84 us against 82, B16 h16 d64
-// S512 170 against 167.
-constexpr int kLongSeq = 1024;
+// Head dim 128, LONG from this length on: one stationary pair and four moving
+// ones instead of two and two (shared memory holds six), which a short item does
+// not repay.  B8 h8, us, float16: S 192 30.0 against 28.1, 384 52.1 and 51.4, 512
+// 75.8 and 76.3; bfloat16: S 1024 183 and 201, 1536 361 and 419.
+// At head dims up to 64 two buffers of scores and two sets of sums, so that the
+// next item starts while one is written out, lost to three buffers from S 129 on
+// (B16 h16 S129 45.2 against 46.8 us, S512 151 and 157; B8 h16 S1536 436 and 488).
+constexpr int kLongSeq = 512;
 constexpr int kBwdThreads = 480;
 constexpr int kPauseLoad = 50, kPauseSoft = 20, kPauseStore = 200;   // ns between polls
 
@@ -829,8 +830,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   uint64_t* bar = reinterpret_cast<uint64_t*>(sChains + 8 * kChains * kChain);
   uint64_t *st_full = bar, *st_empty = st_full + C::kSlots, *mv_full = st_empty + C::kSlots,
            *mv_empty = mv_full + C::kNs, *s_full = mv_empty + C::kNs, *p_full = s_full + C::kFull, *s_free = p_full + C::kBuf,
-           *acc_full = s_free + C::kBuf, *acc_free = acc_full + C::kAcc;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(acc_free + C::kAcc);
+           *acc_full = s_free + C::kBuf, *acc_free = acc_full + 1;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(acc_free + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* err = g_attention_err;
@@ -839,7 +840,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     for (int i = 0; i < C::kFull; ++i) mbar_init(&s_full[i], 2);
     for (int i = 0; i < C::kBuf; ++i) mbar_init(&p_full[i], 4), mbar_init(&s_free[i], 1);
     for (int i = 0; i < C::kNs; ++i) mbar_init(&mv_full[i], 1), mbar_init(&mv_empty[i], 1);
-    for (int i = 0; i < C::kAcc; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_free[i], 4);
+    mbar_init(acc_full, 1), mbar_init(acc_free, 4);
     fence_barrier_init();
   }
   if (warp == 13) tmem_alloc(tslot, 512);
@@ -1009,17 +1010,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int ms = g % C::kNs, w = g % C::kBuf;
         if (!wait_bar<0>(&p_full[w], (g / C::kBuf) & 1, err, 311)) break;
         const TileInfo t = *info_of(g);
-        const int ab = t.item % C::kAcc;
-        if ((t.bits & kFirst) && !wait_bar<0>(&acc_free[ab], ((t.item / C::kAcc) & 1) ^ 1, err, 312)) break;
+        if ((t.bits & kFirst) && !wait_bar<0>(acc_free, (t.item & 1) ^ 1, err, 312)) break;
         if (t.tile < 0) {
           mbar_arrive(&mv_empty[ms]);
           mbar_arrive(&s_free[w]);
           if (t.bits & kEnd) ++ends;
-          else mbar_arrive(&acc_full[ab]);
+          else mbar_arrive(acc_full);
           continue;
         }
         tc_fence_after();
-        const uint32_t acc1 = tmem + C::kSums + ab * 2 * D, acc2 = acc1 + D, tS = tmem + w * 128;
+        const uint32_t acc1 = tmem + C::kSums, acc2 = acc1 + D, tS = tmem + w * 128;
         const uint64_t b1 = dmn + ms * (2 * C::kMv >> 4), b2 = b1 + (C::kMv >> 4);
         const uint32_t more = t.bits & kFirst ? 0u : 1u;
         if (t.bits & kKeys) {
@@ -1030,7 +1030,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int kk = 0; kk < 4; ++kk) mma_f16_ts(acc1, tS + 64 + kk * 8, b1 + kk * 128, id, more | (kk > 0));
         mma_commit(&s_free[w]);
         mma_commit(&mv_empty[ms]);
-        if (t.bits & kLast) mma_commit(&acc_full[ab]);
+        if (t.bits & kLast) mma_commit(acc_full);
       }
     }
   } else if (warp >= 8) {
@@ -1043,12 +1043,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     for (int it = blockIdx.x; it < 2 * items && ok; it += gridDim.x, ++n) {
       const bool keys = it < items;
       const int x = keys ? it : it - items, bh = x / nr, ri = x - bh * nr, b = bh / a.nh, h = bh - b * a.nh;
-      const int slot = n % C::kSlots, ab = n % C::kAcc;
+      const int slot = n % C::kSlots;
       uint8_t* st = sSt + slot * 2 * C::kSt;
       ok = wait_warp<kPauseStore>(&st_full[slot], (n / C::kSlots) & 1, err, 321);
       const bool none = ok && *none_flag(n) != 0;
       const float F = kHoldsDs<T> && ok ? *factor(n) : 1.0f;
-      if (ok && (ok = wait_warp<kPauseStore>(&acc_full[ab], (n / C::kAcc) & 1, err, 322))) {
+      if (ok && (ok = wait_warp<kPauseStore>(acc_full, n & 1, err, 322))) {
         tc_fence_after();
 #pragma unroll 1
         for (int q = 0; q < (keys ? 2 : 1); ++q) {
@@ -1057,7 +1057,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             float v[32];
-            tmem_ld32_nowait(tmem + lo + C::kSums + ab * 2 * D + q * D + c * 32, v);
+            tmem_ld32_nowait(tmem + lo + C::kSums + q * D + c * 32, v);
             tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -1073,7 +1073,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_free[ab]);
+        if (lane == 0) mbar_arrive(acc_free);
         fence_proxy_async_smem();
       }
       // each warp times its own waits: all four go on, or none does
@@ -1548,11 +1548,8 @@ bool attention_tc_bwd_run(int dt, const AttnOp& a, cudaStream_t s) {
     if (a.vec) return h ? bwd_one<half_t, true>(a, s) : bwd_one<bf16_t, true>(a, s);
     return h ? bwd_one<half_t, false>(a, s) : bwd_one<bf16_t, false>(a, s);
   }
-  if (a.S > kLongSeq) {
-    if (a.d <= 64) return h ? bwd<half_t, 64, true>(a, s) : bwd<bf16_t, 64, true>(a, s);
-    return h ? bwd<half_t, 128, true>(a, s) : bwd<bf16_t, 128, true>(a, s);
-  }
   if (a.d <= 64) return h ? bwd<half_t, 64, false>(a, s) : bwd<bf16_t, 64, false>(a, s);
+  if (a.S >= kLongSeq) return h ? bwd<half_t, 128, true>(a, s) : bwd<bf16_t, 128, true>(a, s);
   return h ? bwd<half_t, 128, false>(a, s) : bwd<bf16_t, 128, false>(a, s);
 }
 
