@@ -5,8 +5,9 @@ import math
 import pytest
 import torch
 
+import attention_ref as ref
 import transformer_layer_pre_b200 as tlp
-from test_gpu_attention import DT
+from test_gpu_attention import DT, _check
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +35,55 @@ def test_many_small_probabilities_next_to_a_large_one(dtype, d, first):
     want = rest / (1 + rest)
     assert float((o.double() - want).abs().max()) <= want * (2 * u + (s / 16 + s / 64) * 2.0 ** -23 + 2.0 ** -17)
     assert float((lse.double() - 12.5 - math.log(1 + rest)).abs().max()) <= (s / 64) * 2.0 ** -23 + 16 * 2.0 ** -23 * 13
+
+
+def _finite_masks(dtype, value, s, d):
+    """Masks that remove nothing: over a whole sequence, over its first half (the running reference starts there), and in
+    steps of a quarter of the value (it climbs)."""
+    g = torch.Generator(device="cuda").manual_seed(s)
+    q, k, v, do = (torch.randn(3, s, 2, d, generator=g, device="cuda").to(DT[dtype]) for _ in range(4))
+    table = torch.randn(32, 2, generator=g, device="cuda").to(DT[dtype])
+    m = torch.zeros(3, s, device="cuda")
+    m[0] = value
+    m[1, : s // 2] = value
+    m[2] = value * (1 - (4 * torch.arange(s, device="cuda") // s) / 4)
+    return q, k, v, do, m, table
+
+
+FINITE = [(dt, x, s, d) for dt in ("f32", "f16", "bf16") for x in (-1e4, -1e6, -3e7, -1e8, -1e9, -1e29)
+          for s, d in ((100, 64), (600, 64), (300, 128))]
+
+
+@pytest.mark.parametrize("dtype,value,s,d", FINITE)
+def test_forward_under_finite_masks(dtype, value, s, d):
+    """Within the bounds, which grow with |mask|, and finite."""
+    q, k, v, _, m, table = _finite_masks(dtype, value, s, d)
+    for t in (None, table):
+        o, lse = tlp.attention_forward(q, k, v, m, t)
+        tlp.device_check()
+        assert bool(torch.isfinite(o).all()) and bool(torch.isfinite(lse).all())
+        want, tol = ref.forward(q, k, v, m, t)
+        _check("o", o, want["o"], tol["o"])
+        _check("lse", lse, want["lse"], tol["lse"])
+        # a float32 lse holds log2 of the sum to half a last place of its own size, whatever the reference was
+        whole = lse[0].double() - value
+        assert float((whole - (want["lse"][0] - value)).abs().max()) <= 16 * 2.0 ** -24 * abs(value) + 2.0 ** -17
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_that_float32_rounds_by_whole_units(dtype, d):
+    """Scores of 2^21 to 2^27 with steps between the keys, and a bias: P stays finite in float16."""
+    g = torch.Generator(device="cuda").manual_seed(d)
+    s = 520
+    for size in (2.0 ** 21, 2.0 ** 24, 2.0 ** 27):
+        q = torch.full((1, s, 2, d), 64.0, device="cuda")
+        k = (size / (64 * d)) * (1 + torch.arange(s, device="cuda") / s * 2.0 ** -9)[None, :, None, None].expand(1, s, 2, d)
+        v = torch.randn(1, s, 2, d, generator=g, device="cuda")
+        table = 3 * torch.randn(32, 2, generator=g, device="cuda")
+        q, k, v, table = (t.to(DT[dtype]).contiguous() for t in (q, k, v, table))
+        for t in (None, table):
+            o, lse = tlp.attention_forward(q, k, v, None, t, scale=1.0)
+            tlp.device_check()
+            assert bool(torch.isfinite(o).all()) and bool(torch.isfinite(lse).all())
+            assert float(o.abs().max()) <= float(v.abs().max()) * (1 + 2.0 ** -6)

@@ -54,6 +54,15 @@ template <> __device__ __forceinline__ uint32_t pack2<bf16_t>(float lo, float hi
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// The same for probabilities, which scores so large that float32 rounds them by
+// whole units (from 2^23) may bring above float16's end: kept finite.
+template <typename T> __device__ __forceinline__ uint32_t pack_p(float lo, float hi) { return pack2<T>(lo, hi); }
+template <> __device__ __forceinline__ uint32_t pack_p<half_t>(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // Bounded wait on an mbarrier that pauses between its polls: polls go through
 // the shared memory that the products read their operands from (a tight loop
 // of polls in every waiting warp made the backward 14 % slower).
@@ -193,14 +202,13 @@ struct LiveTiles {
 // thread; 4: TMA; 5: MMA.  TMEM: S, P over S once it is read, O.
 //
 // Online softmax with a lazy reference: P = 2^(x - ref), ref the row maximum
-// when O was last rescaled; O and the row sum are rescaled only once the
-// maximum has grown by more than 2^8, so P stays below 256 and most tiles
-// skip it.  P is rounded to the storage type (at most half a step, relative)
-// for its product with V; the row sum takes the unrounded P.  P and the row sum
-// are held 2^7 times too large (exact; O / l does not see it, lse takes it out):
-// float16's subnormals, whose rounding is absolute, then begin at 2^-21 of the
-// row's maximum instead of 2^-14, and what 2^20 small probabilities lose there
-// is at most 2^-12 of the largest |V|.
+// when O was last rescaled, less 7; O and the row sum are rescaled only once the
+// maximum has grown by more than 2^8, so P stays below 2^15 and most tiles skip
+// it.  P is rounded to the storage type (at most half a step, relative) for its
+// product with V; the row sum takes the unrounded P.  The 7: float16's subnormals,
+// whose rounding is absolute, begin at 2^-21 of the row's maximum instead of
+// 2^-14, and what 2^20 small probabilities lose there is at most 2^-12 of the
+// largest |V|.  O / l does not see it, and lse takes ref as it was used.
 //
 // The bias is one number for a tile beyond the last bucket's border; else the
 // tile's 255 diagonals are staged as four copies shifted by one float each, so
@@ -233,7 +241,7 @@ struct Fwd {
 static_assert(4 * (Fwd<64>::kSmem + 1024) <= 228 * 1024 && 2 * (Fwd<128>::kSmem + 1024) <= 228 * 1024,
               "the blocks of an SM do not fit its shared memory");
 constexpr int kFwdThreads = 192;
-constexpr float kRescale = 8.0f, kFwdUp = 7.0f;   // log2: P < 2^15 in float16
+constexpr float kRescale = 8.0f, kFwdUp = 7.0f;   // log2
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
@@ -526,17 +534,17 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
         if (lane == 0) mbar_arrive(&aux_empty[as]);
         const float top = fmaf(fmaxf(m0, m1), mul, add);
         // O holds the products of every tile before: they were issued ahead of this Q K^T
-        const float mnew = fmaxf(ref, top);
         if (t.bits & kFirst) {
-          ref = mnew;
-        } else if (__any_sync(0xffffffffu, mnew > ref + kRescale)) {
-          const float f = mnew > ref + kRescale ? ex2f(ref - mnew) : 1.0f;
-          if (f != 1.0f) ref = mnew;
+          ref = top - kFwdUp;
+        } else if (__any_sync(0xffffffffu, top - ref > kFwdUp + kRescale)) {
+          const float next = top - kFwdUp;
+          const float f = top - ref > kFwdUp + kRescale ? ex2f(ref - next) : 1.0f;
+          if (f != 1.0f) ref = next;
           l *= f;
 #pragma unroll 1
           for (int c = 0; c < D; c += 8) tmem_scale8(tmem + lo + C::kO + c, f);
         }
-        const float sub = add - (ref == -INFINITY ? 0.0f : ref) + kFwdUp;
+        const float sub = add - (ref == -INFINITY ? 0.0f : ref);
         float2 sum0 = f2(0.0f), sum1 = f2(0.0f);
 #pragma unroll 1
         for (int c = 0; c < C::kTK / 32; ++c) {
@@ -550,7 +558,7 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
             const float2 p = make_float2(ex2f(y.x), ex2f(y.y));
             if (e & 1) sum1 = __fadd2_rn(sum1, p);
             else sum0 = __fadd2_rn(sum0, p);
-            w[e] = pack2<T>(p.x, p.y);
+            w[e] = pack_p<T>(p.x, p.y);
           }
           // over S columns that this thread has read
           tmem_st16u(tmem + lo + c * 16, w);
@@ -589,7 +597,7 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
         }
         tc_fence_before();
         const int row = i * 128 + r;
-        if (row < a.S) a.lse[(size_t)bh * a.S + row] = l == 0.0f ? INFINITY : (ref + (log2f(l) - kFwdUp)) * kAttnLn2;
+        if (row < a.S) a.lse[(size_t)bh * a.S + row] = l == 0.0f ? INFINITY : (ref + log2f(l)) * kAttnLn2;
         fence_proxy_async_smem();
       }
       // each warp times its own waits: all four go on, or none does
