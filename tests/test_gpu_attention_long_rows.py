@@ -87,3 +87,46 @@ def test_scores_that_float32_rounds_by_whole_units(dtype, d):
             tlp.device_check()
             assert bool(torch.isfinite(o).all()) and bool(torch.isfinite(lse).all())
             assert float(o.abs().max()) <= float(v.abs().max()) * (1 + 2.0 ** -6)
+
+
+@pytest.mark.parametrize("dtype,value,s,d", FINITE)
+def test_backward_under_finite_masks(dtype, value, s, d):
+    """Finite, and within the bounds, which grow with |mask| and |lse|: where a place of lse is worth more than a factor
+    of the probabilities they bound nothing else."""
+    q, k, v, do, m, table = _finite_masks(dtype, value, s, d)
+    for t in (None, table):
+        o, lse = tlp.attention_forward(q, k, v, m, t)
+        grads = dict(zip(("dq", "dk", "dv", "dtable"), tlp.attention_backward(q, k, v, o, lse, do, m, t)))
+        tlp.device_check()
+        if t is None:
+            assert grads.pop("dtable") is None
+        for name, x in grads.items():
+            assert bool(torch.isfinite(x).all()), name
+        want, tol = ref.backward(q, k, v, o, lse, do, m, t)
+        for name, x in grads.items():
+            _check(name, x, torch.nan_to_num(want[name], 0.0, 0.0, 0.0), torch.nan_to_num(tol[name], math.inf, math.inf))
+        # the sequence that masks only its first half (and its gradients) is as if those keys were removed
+        if value <= -1e6:
+            gone = m[1:2].clone()
+            gone[gone < 0] = -math.inf
+            one = [x[1:2].contiguous() for x in (q, k, v)]
+            o1, lse1 = tlp.attention_forward(*one, gone, t)
+            want = tlp.attention_backward(*one, o1, lse1, do[1:2].contiguous(), gone, t)
+            tlp.device_check()
+            assert float((o[1:2] - o1).abs().max()) <= 2 * torch.finfo(o1.dtype).eps * float(o1.abs().max())
+            for name, y in zip(("dq", "dk", "dv"), want):
+                assert float((grads[name][1:2].double() - y.double()).abs().max()) <= 2.0 ** -6 * float(y.double().abs().max())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("s,d", [(100, 64), (300, 128)])
+def test_gradients_are_finite_under_any_finite_mask(dtype, s, d):
+    """A whole row masked by a finite value: among them ones whose lse, rounded, lies a place below the scores."""
+    g = torch.Generator(device="cuda").manual_seed(s)
+    q, k, v, do = (torch.randn(1, s, 2, d, generator=g, device="cuda").to(DT[dtype]) for _ in range(4))
+    for value in [-1.36e8, -1.41e8] + [-10.0 ** (4 + 0.1 * i + 0.001 * j) for i in range(259) for j in (0, 37)]:
+        m = torch.full((1, s), value, device="cuda")
+        o, lse = tlp.attention_forward(q, k, v, m)
+        grads = tlp.attention_backward(q, k, v, o, lse, do, m)[:3]
+        assert all(bool(torch.isfinite(x).all()) for x in (o, *grads)), value
+    tlp.device_check()

@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(const __grid_co
       const int x = (i >> 6) * 128 + (i & 63);
       constexpr float up = sizeof(T) == 2 ? kAttnPUp : 1.0f, up2 = sizeof(T) == 2 ? 8.0f : 0.0f;   // and its log2
       static_assert(kAttnPUp == 256.0f, "up2 is its logarithm");
-      st[x] = up2 - lse * kAttnLog2e;
+      st[x] = up2 - lse_log2(lse);
       st[x + 64] = i < a.S ? -t[k] * (1.0f / up) : 0.0f;
     }
     if (kMax && i < a.S) {

@@ -70,6 +70,15 @@ __device__ __forceinline__ __half2 warp_max2(__half2 m) {
   for (int o = 16; o > 0; o >>= 1) m = __hmax2(m, __shfl_xor_sync(0xffffffffu, m, o));
   return m;
 }
+// lse in log2 units, for P = 2^(x - lse2).  Both come through some six roundings
+// of their own size; where those are worth more than a factor (|lse2| above
+// 2^21: finite masks over a whole row, -1e8 and the like), P is not known, and
+// lse2 is raised by eight of them, so that P stays below 1 instead of passing
+// the storage type's end.
+__device__ __forceinline__ float lse_log2(float lse) {
+  const float x = lse * kAttnLog2e, slack = fabsf(x) * (1.0f / (1 << 20));
+  return slack > 2.0f ? x + slack : x;
+}
 // 1 / x of a power of two.
 __device__ __forceinline__ float inv_pow2(float x) { return __int_as_float((254 << 23) - __float_as_int(x)); }
 

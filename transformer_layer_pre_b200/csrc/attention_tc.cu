@@ -1329,7 +1329,7 @@ __global__ void __launch_bounds__(One::kThreads, 2)
       }
     }
     d += __shfl_xor_sync(0xffffffffu, d, 1);
-    if (part) vecA[row] = row < a.S ? 8.0f - lse * kAttnLog2e : -INFINITY;
+    if (part) vecA[row] = row < a.S ? 8.0f - lse_log2(lse) : -INFINITY;
     else vecB[row] = -d * (1.0f / kAttnPUp);
     if (kHoldsDs<T>) {
       // a sequence with a key has no empty row; rows past the end were read as 0
