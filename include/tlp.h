@@ -302,8 +302,8 @@ tl_status tl_bias_grad_noalloc(int dtype, const void* dz, int rows, int cols, fl
  * left gets O = 0 and lse = +inf, and its gradients are 0; a removed key
  * weighs 0 in every product, so its K, V, Q, dO must be finite.  Other values are
  * added as they are, with float32's rounding of the sum: over a whole row, -1e4
- * costs three digits of the softmax, and from about -1e6 on lse no longer tells
- * the probabilities apart (gradients stay finite).  lse and O given to the
+ * leaves about three digits of the softmax, and from about -1e6 on lse no longer
+ * tells the probabilities apart (gradients stay finite).  lse and O given to the
  * backward are those of the forward.
  *
  * tl_heads: a (batch, seq, heads, head_dim) tensor by its element strides;
