@@ -753,8 +753,11 @@ __device__ __forceinline__ void bin_diagonals(const float* chains, const uint8_t
 
 // A tile's scores and dP, 64 columns of this thread's row, into P and dS.
 // ax: the tile's staged vectors; row: what this row adds (log2 units, bias of
-// a far tile included), nd_row: -D of a query row, F / kAttnPUp in it; up: F /
-// kAttnPUp, with F the factor that dS is held at (ds_factor; 1 for bfloat16).
+// a far tile included).  With F the factor that dS is held at (ds_factor; none
+// for bfloat16): nd_row: -D F / kAttnPUp of a query row, up: F / kAttnPUp there,
+// F for keys, whose column vector -D / kAttnPUp does not hold it (P times F took
+// 287 us where the vector times F, with more values alive, took 306: B4 h8 d128
+// S2048).
 template <typename T, bool KEYS, bool NEAR, bool MIX>
 __device__ __forceinline__ void bwd_tile(uint32_t tS, const uint8_t* ax, int win, const float* vecA, const float* vecB,
                                          float c2, float row, float nd_row, float up, int r, bool grad, float& far_sum,
@@ -781,10 +784,6 @@ __device__ __forceinline__ void bwd_tile(uint32_t tS, const uint8_t* ax, int win
         const float4 w = *reinterpret_cast<const float4*>(vecB + c * 32 + e);
         nd0 = make_float2(w.x, w.y);
         nd1 = make_float2(w.z, w.w);
-        if (kHoldsDs<T>) {
-          nd0 = __fmul2_rn(nd0, f2(up * kAttnPUp));
-          nd1 = __fmul2_rn(nd1, f2(up * kAttnPUp));
-        }
       }
       if (NEAR) {
         const float4 w = *reinterpret_cast<const float4*>(wnd + c * 32 + e);
@@ -794,8 +793,11 @@ __device__ __forceinline__ void bwd_tile(uint32_t tS, const uint8_t* ax, int win
       const float2 x0 = __ffma2_rn(make_float2(s[e], s[e + 1]), f2(c2), add0);
       const float2 x1 = __ffma2_rn(make_float2(s[e + 2], s[e + 3]), f2(c2), add1);
       const float2 p0 = make_float2(ex2f(x0.x), ex2f(x0.y)), p1 = make_float2(ex2f(x1.x), ex2f(x1.y));
-      const float2 d0 = __fmul2_rn(p0, __ffma2_rn(make_float2(dp[e], dp[e + 1]), f2(up), nd0));
-      const float2 d1 = __fmul2_rn(p1, __ffma2_rn(make_float2(dp[e + 2], dp[e + 3]), f2(up), nd1));
+      float2 g0 = p0, g1 = p1;
+      if (KEYS && kHoldsDs<T>) g0 = __fmul2_rn(p0, f2(up)), g1 = __fmul2_rn(p1, f2(up));
+      const float m = KEYS || !kHoldsDs<T> ? 1.0f / kAttnPUp : up;
+      const float2 d0 = __fmul2_rn(g0, __ffma2_rn(make_float2(dp[e], dp[e + 1]), f2(m), nd0));
+      const float2 d1 = __fmul2_rn(g1, __ffma2_rn(make_float2(dp[e + 2], dp[e + 3]), f2(m), nd1));
       if (KEYS) {
         wp[e / 2] = pack2<T>(p0.x, p0.y);
         wp[e / 2 + 1] = pack2<T>(p1.x, p1.y);
@@ -1153,7 +1155,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         nd = keys ? 0.0f : rv[(r >> 6) * 128 + 64 + (r & 63)];
         if (kHoldsDs<T>) {
           const float F = *factor(cur);
-          up = F * (1.0f / kAttnPUp);
+          up = keys ? F : F * (1.0f / kAttnPUp);
           nd *= F;
         }
         grad = want && !keys;
