@@ -25,3 +25,14 @@ def test_no_warp_leaves_between_its_last_wait_and_the_barrier(begin):
     at = code.index(begin)
     part = code[at:code.index("named_barrier_all", at)]
     assert "break" not in part and "return" not in part and "continue" not in part
+
+
+def test_pairs_of_warps_of_the_long_layer_attention_leave_together():
+    code = _code("attn_tc.cu")
+    at = code.index("const int bar_id = 1 + quarter;")
+    part = code[at:code.index("tmem_dealloc", at)]
+    assert len(re.findall(r"ok = named_barrier_all\(bar_id, 64, true\)\)\) break;", part)) == 2
+    # a wait that ran out leads to one of these barriers before the warp leaves
+    waits = re.findall(r"mbar_wait_warp\([^;]*\)\) (.*)", part)
+    assert len(waits) == 5 and all(w.startswith("{ gave_up(); break; }") for w in waits)
+    assert len(re.findall(r"[^_]named_barrier\(bar_id, 64\)", part)) == 1

@@ -368,6 +368,9 @@ __global__ void __launch_bounds__(kLThreads, 1)
     float* xch = reinterpret_cast<float*>(tslot + 4);   // [2 tiles][2 halves][128] row maxima, then row sums
     uint32_t g = 0;
     bool ok = true;
+    // a warp whose wait ran out meets the other of its pair once more, at whatever
+    // barrier that one comes to next, and both leave
+    auto gave_up = [&] { named_barrier_all(bar_id, 64, false); };
     for (int it = blockIdx.x; it < nitems && ok; it += gridDim.x) {
       const int bh = it / nq, q0 = (it - bh * nq) * TILE;
       const int b = bh / a.nh, h = bh - b * a.nh;
@@ -378,9 +381,9 @@ __global__ void __launch_bounds__(kLThreads, 1)
         const int ss = g & 1;
         const uint8_t* ax = saux + ss * kLAux;
         const float* mrow = reinterpret_cast<const float*>(ax + 2048) + hf * 64;
-        if (!(ok = mbar_wait_warp(&aux_full[ss], (g >> 1) & 1, a.err, 88))) break;
+        if (!(ok = mbar_wait_warp(&aux_full[ss], (g >> 1) & 1, a.err, 88))) { gave_up(); break; }
         const uint2 kb8 = a.drop.thr ? *reinterpret_cast<const uint2*>(ax + r * 16 + hf * 8) : make_uint2(~0u, ~0u);
-        if (!(ok = mbar_wait_warp(&s_full[ss], (g >> 1) & 1, a.err, 89))) break;
+        if (!(ok = mbar_wait_warp(&s_full[ss], (g >> 1) & 1, a.err, 89))) { gave_up(); break; }
         tc_fence_after();
         const uint32_t ts = tmem + 128 * ss + lo + hf * 64;
         float sv[64];
@@ -396,7 +399,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
           mx = max3f(mx, max3f(x0.x, x0.y, x1.x), x1.y);
         }
         xch[(ss * 2 + hf) * 128 + r] = mx;
-        named_barrier(bar_id, 64);
+        if (!(ok = named_barrier_all(bar_id, 64, true))) break;
         mx = fmaxf(xch[(ss * 2) * 128 + r], xch[(ss * 2 + 1) * 128 + r]);
         const float mnew = fmaxf(mref, mx);
         if (j == 0) {
@@ -405,7 +408,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
           const bool need = mnew > mref + kLRescale;
           if (__any_sync(0xffffffffu, need)) {
             // O (and the row sum) to the new reference, once the previous product is in
-            if (!(ok = mbar_wait_warp(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, a.err, 90))) break;
+            if (!(ok = mbar_wait_warp(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, a.err, 90))) { gave_up(); break; }
             tc_fence_after();
             const float alpha = need ? ex2_approx(mref - mnew) : 1.0f;
             float o[32];
@@ -422,7 +425,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
         }
         const float msub = mref == -INFINITY ? 0.0f : mref;   // 2^(-inf - msub) = 0
         // the P slot is free once the product of tile g-2 is done
-        if (g >= 2 && !(ok = mbar_wait_warp(&pv_done[ss], ((g - 2) >> 1) & 1, a.err, 91))) break;
+        if (g >= 2 && !(ok = mbar_wait_warp(&pv_done[ss], ((g - 2) >> 1) & 1, a.err, 91))) { gave_up(); break; }
         // pass 2: P = 2^(x - m_ref), dropped, into this half of the P tile;
         // row sum of the undropped P (the S values are still in registers)
         float2 ls2 = make_float2(0.0f, 0.0f);
@@ -453,12 +456,12 @@ __global__ void __launch_bounds__(kLThreads, 1)
       // the item's output once its last product is in: this thread's 32
       // columns of the row; the row sum is the two halves' sums
       const uint32_t gl = g - 1;
-      if (!(ok = mbar_wait_warp(&pv_done[gl & 1], (gl >> 1) & 1, a.err, 92))) break;
+      if (!(ok = mbar_wait_warp(&pv_done[gl & 1], (gl >> 1) & 1, a.err, 92))) { gave_up(); break; }
       tc_fence_after();
       float o[32];
       tmem_ld32(tmem + 256 + lo + hf * 32, o);
       xch[(512 + hf * 128) + r] = l;
-      named_barrier(bar_id, 64);
+      if (!(ok = named_barrier_all(bar_id, 64, true))) break;
       const float lt = xch[512 + r] + xch[640 + r];
       named_barrier(bar_id, 64);   // both have read the sums before the next item's tile maxima land
       const float inv = lt > 0.0f ? dsc / lt : 0.0f;
