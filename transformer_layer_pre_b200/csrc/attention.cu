@@ -22,7 +22,10 @@ namespace {
 // blocks that clear dpart, and blocks of prep_rows(G) * 256 / G tokens of one
 // sequence and head for stats (and, float16, smax), G lanes per row reading 16
 // bytes each.
-// Bound: launch latency (3 us) in the forward and where the backward forms D itself.
+// Bound: launch latency (3 us) in the forward and where the backward forms D
+// itself; else the latency of a group's loads: O and dO of B16 h16 d64 S512, 33.6
+// MB, 15 us (2.2 TB/s), with V of float16, 50.3 MB, 18 us.  Eight rows in flight
+// per group made a whole backward 6 % slower.
 template <typename T, int G>
 __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(const __grid_constant__ AttnOp a, int nmask, int nvec, int nzero) {
   pdl_wait();
@@ -152,8 +155,8 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(const __grid_co
 
 // dtable[u, h] (+)= sum over sequences and items of dpart, in a fixed order
 // and in float64: a block per head and 32 buckets, a lane per bucket (whole
-// lines of dpart), the rows dealt to the warps.  Bound: latency; 3.5 us for 64 rows
-// per head of 16 heads and 32 buckets, 5.8 for 512.
+// lines of dpart), the rows dealt to the warps.  Bound: latency; 4 us for 64 rows per
+// head of 16 heads and 32 buckets, 6 for 512.
 constexpr int kTableWarps = 32;
 __global__ void __launch_bounds__(32 * kTableWarps) attn_table_grad_kernel(const __grid_constant__ AttnOp a) {
   __shared__ double red[kTableWarps][33];

@@ -115,7 +115,6 @@ struct AttnOp {
   int daccumulate;
   // bucket u holds the diagonals j - i in [lo[u], lo[u] + n[u]) (n = 0: none)
   int lo[kAttnMaxBuckets], n[kAttnMaxBuckets];
-  int* err;
 };
 
 // The bias of diagonal x = j - i (direction 0) or x = i - j (direction 1), in

@@ -217,11 +217,12 @@ struct LiveTiles {
 //
 // Bound: the special-function unit (16 exponentials per clock and SM against
 // 128 x 64 of them per tile) and the latency of a tile's chain product -> maximum
-// -> exponentials -> product.  B4 h16 d64 S2048: 138 us, 498 TFLOP/s (0.30 of the
-// measured GEMM rate), exponentials 52 % of their unit's rate, tensor pipe 26 %;
-// h8 d128: 95 us, 721 TFLOP/s; B64 h16 S128, 67.6 MB: 21 us, 3.2 TB/s.
-// Per 128 x 64 tile: two blocks of 128-key tiles on an SM took 168 us, four of 64
-// keys 146; windows read straight from global memory 159.
+// -> exponentials -> product.  B4 h16 d64 S2048: 128 us a call (L2 warm; 138 cold),
+// 537 TFLOP/s (0.32 of the measured GEMM rate), exponentials 52 % of their unit's
+// rate, tensor pipe 26 %; h8 d128: 94 us, 731 TFLOP/s; B64 h16 S128, 67.6 MB: 21
+// us cold, 3.2 TB/s.
+// Per 128 x 64 tile, when first built: two blocks of 128-key tiles on an SM took
+// 168 us, four of 64 keys 146; windows read straight from global memory 159.
 template <int D>
 struct Fwd {
   static constexpr int kTK = D == 64 ? 64 : 128;                    // keys per tile
@@ -645,9 +646,9 @@ __global__ void __launch_bounds__(kFwdThreads, Fwd<D>::kBlocks)
 //
 // Bound: the chain of a tile (operands, product, exponentials, product) through
 // the barriers between its warps: tensor pipe 33 %, exponentials 38 %, issue
-// slots 40 % busy.  B4 h16 d64 S2048: 363 us, 473 TFLOP/s of the 5 products that
-// the formulas have (662 of the 7 formed); h8 d128: 290 us, 593 TFLOP/s; B16 h16
-// S512 padded: 150 us.
+// slots 41 % busy.  A call (L2 warm), B4 h16 d64 S2048: 368 us, 467 TFLOP/s of the
+// 5 products that the formulas have (654 of the 7 formed); h8 d128: 287 us, 599
+// TFLOP/s; B16 h16 S512: 148 us.
 constexpr int kRun = 192, kWin = 200;           // diagonals of a 128 x 64 tile, floats of a window copy
 constexpr int kVecs = 4 * kWin * 4;             // column vectors after the four copies
 constexpr int kChain = 40;                      // floats of a diagonal chain
@@ -1213,10 +1214,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // queries.  Head dim 128 would leave room for one block only and takes the
 // kernel above.
 //
-// Bound: HBM (five tiles in, three out; rows of 128 bytes) behind the latency of
-// a pair's load, two rounds of products and write: B64 h16 S128, 134.7 MB, 41 us,
-// 3.2 TB/s; loads and stores alone 26 us.  The kernel above took 57 us there, and
-// 14 more for D in the prepared workspace.  One block walking several pairs (the
+// Bound: the latency of a pair's load, two rounds of products and write, which two
+// blocks on an SM do not hide (HBM at 27 % of its peak): B64 h16 S128, 134.7 MB,
+// 43 us, 3.1 TB/s; loads and stores alone 26 us.  The kernel above took 57 us
+// there, and 14 more for D in the prepared workspace.  One block walking several pairs (the
 // next V and O loaded ahead, prefetched to L2, or dQ written straight to its rows
 // so that Q, K and dO load ahead too) came to the same or 2 us more.
 //

@@ -12,13 +12,16 @@
 // the second launch ends after the sum.
 //
 // Squares are float64: a float32 square overflows from |g| = 1.8e19 and
-// vanishes below 1e-23, and the conversions and FP64 FMAs (one each per
-// value) stay below the rate at which HBM delivers values.
+// vanishes below 1e-23, and the conversions and FP64 FMAs (one each per value)
+// stay below the rate at which HBM delivers float32 values.  16-bit values come
+// twice as fast, and there the conversions begin to count: 302 M values, the norm
+// alone 206 us of float32 (5.9 TB/s) and 120 us of 16 bits (5.0 TB/s).
 // Bound: HBM; the norm has to be known before anything is scaled, so what
 // exceeds L2 is read twice and written once.  24 layers of hidden 1024 (302 M
 // float32, 2.42 GB read and written once): 608 us, three passes at 5.97 TB/s,
-// 0.91 of the measured copy rate.  108 odd bf16 tensors, 98 MB, out of place: 30 us
-// on the device, and the 108 tensors' checks and addresses 45 us on the host.
+// 0.91 of the measured copy rate; the same number of 16-bit values 312 us, 5.8
+// TB/s.  108 odd bf16 tensors, 98 MB, out of place: 27 us
+// on the device (the norm's read from HBM, the scaling's from L2), and the 108 tensors' checks and addresses 45 us on the host.
 #include <cuda_runtime.h>
 
 #include <math.h>
