@@ -102,6 +102,18 @@ def test_random_views(lib):
     assert 200 < refused < 1300
 
 
+@pytest.mark.parametrize("odd", [0, -1, 3, (1 << 63) - 1, -(1 << 63)])
+def test_strides_of_single_entries_mean_nothing(lib, odd):
+    desc = _desc(batch=1, heads=1)
+    at, _, lse, ws = _far()
+    strides = [(odd, D, odd)] * 8
+    at[3] = at[0] + 5 * D * ES
+    assert _call(lib, desc, at, strides, lse, ws, backward=False) == EINVAL
+    if not torch.cuda.is_available():          # else it would run on made-up addresses
+        at[3] = at[0] + S * D * ES
+        assert _call(lib, desc, at, strides, lse, ws, backward=False) != EINVAL
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("form", ["tokens", "heads", "sequences"])

@@ -19,7 +19,8 @@ struct ByteRows {
   // (batch, token, head, head_dim) entries of es bytes by element strides
   ByteRows(const void* p, int64_t sb, int B, int64_t st, int S, int64_t sh, int nh, int d, int es)
       : ByteRows(p, (int64_t)d * es) {
-    Dim x[3] = {{sb * es, B}, {st * es, S}, {sh * es, nh}};
+    // the stride of a dimension of one entry means nothing and may hold anything
+    Dim x[3] = {{B > 1 ? sb * es : 0, B}, {S > 1 ? st * es : 0, S}, {nh > 1 ? sh * es : 0, nh}};
     std::sort(x, x + 3, [](const Dim& l, const Dim& r) { return l.stride < r.stride; });
     for (const Dim& e : x) {
       if (e.count == 1) continue;
